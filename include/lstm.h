@@ -240,6 +240,76 @@ lstm_status lstm_forward_noalloc(const lstm_desc* desc, const void* x, const voi
  * reports an error.  No counterpart on the pages (see lstm_forward_noalloc). */
 lstm_status lstm_noalloc_query_status(cudaStream_t stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Operators beside the LSTM.  The pages define no counterpart; they are what
+ * training and serving a stack of recurrent layers needs next to the layers.
+ * Ownership, streams, graph capture and errors are those of the LSTM calls:
+ * caller-owned device buffers, stream-ordered work only, arguments checked
+ * on the host before anything is enqueued.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * AdamW over all tensors of a model (Loshchilov and Hutter 2019).  With
+ * t = *step + 1, g the gradient times scalars[1] and lr times scalars[0]
+ * (factors 1 when scalars is NULL), per element in float32:
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * then *step = t.  The step counter and the factors live on the device, so a
+ * captured call counts its steps and follows a schedule when it is replayed.
+ * Host arrays of num_tensors device pointers:
+ *   numel       elements of each tensor (>= 0);
+ *   param       float32 parameters, updated in place;
+ *   param_bf16  NULL, or bf16 copies of the updated parameters (rounded to
+ *               nearest even) for layers that compute in bf16; entries may
+ *               be NULL;
+ *   grad        gradients, grad_dtype;
+ *   m, v        state_bits 32: float32 moments.  state_bits 8: int8 codes c
+ *               of m, standing for sign(c) (c/127)^2 a, and uint8 codes of v,
+ *               standing for (c/255)^4 a, where a is the scale of the
+ *               element's block of 256 consecutive elements of the tensor;
+ *   m_scale, v_scale  state_bits 8: ceil(numel / 256) float32 scales each;
+ *               ignored (may be NULL) for 32.
+ * 8-bit moments are zero when codes and scales are zero.  A scale is its
+ * block's largest magnitude; codes are rounded up or down at random with the
+ * probability that keeps the mean of the value, by 16 random bits that are a
+ * function of (seed, t, tensor index, element index) alone, so a run repeats
+ * bit for bit; a second moment that is not zero keeps a code of at least 1.
+ * A block whose moments hold a NaN or an infinity gets a NaN scale; one whose
+ * largest magnitude is below 2^-126 becomes zero.
+ * The tensors must not overlap.  A tensor with numel 0 is skipped; its
+ * entries may be NULL.  With num_tensors 0 only the step counter moves.
+ * LSTM_ERR_INVALID_ARG: a NULL array or entry, a pointer off its type's
+ * alignment, state_bits other than 8 or 32, lr, eps or weight_decay negative
+ * or not finite, eps 0, beta1 or beta2 outside [0, 1).
+ */
+typedef struct {
+    int num_tensors;
+    lstm_dtype grad_dtype;
+    int state_bits;
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;
+    double weight_decay;
+    unsigned long long seed;   /* of the 8-bit rounding */
+} lstm_adamw_desc;
+
+lstm_status lstm_adamw_step(const lstm_adamw_desc* desc, const long long* numel, float* const* param,
+                            void* const* param_bf16, const void* const* grad, void* const* m, void* const* v,
+                            float* const* m_scale, float* const* v_scale, long long* step,
+                            const float* scalars, cudaStream_t stream);
+
+/* The moments of an 8-bit state as float32 values (for a checkpoint, or to
+ * look at them): m_out, v_out are host arrays of num_tensors device pointers
+ * to numel float32 values each.  desc->state_bits must be 8. */
+lstm_status lstm_adamw_read_state(const lstm_adamw_desc* desc, const long long* numel, void* const* m,
+                                  void* const* v, float* const* m_scale, float* const* v_scale,
+                                  float* const* m_out, float* const* v_out, cudaStream_t stream);
+
 /* Synchronises `stream` and returns the kernel-side status recorded in
  * `workspace` by the last call that used it (LSTM_OK or LSTM_ERR_TIMEOUT), or
  * LSTM_ERR_CUDA if the stream reports an error.  A kernel's inter-block or
@@ -263,7 +333,7 @@ const char* lstm_status_string(lstm_status status);
  * engine: _tc tensor cores, _ffma / _simt CUDA cores): pack, proj_gemm_tc,
  * proj_gemm_simt, fwd_rec_tc, fwd_rec_ffma, bwd_rec_tc, bwd_rec_ffma,
  * dw_gemm_tc, dw_gemm_simt, dx_gemm_tc, dx_gemm_simt, db_reduce, seq_copy,
- * transpose, dropout.
+ * transpose, dropout, adamw.
  * lstm_timing_reset
  * zeroes the totals.  Process-wide and thread-safe; event recording adds a
  * few microseconds per launch, so leave it off outside measurements.

@@ -24,7 +24,8 @@ LSTM_BF16 = 1
 EXPORTED = ("lstm_workspace_size", "lstm_reserve_size", "lstm_forward", "lstm_backward",
             "lstm_query_status", "lstm_status_string", "lstm_timing_enable", "lstm_timing_read",
             "lstm_timing_reset", "lstm_forward_noalloc", "lstm_trace_enable", "lstm_trace_read",
-            "lstm_forward_varlen", "lstm_backward_varlen", "lstm_noalloc_query_status")
+            "lstm_forward_varlen", "lstm_backward_varlen", "lstm_noalloc_query_status", "lstm_adamw_step",
+            "lstm_adamw_read_state")
 LSTM_NOALLOC_SCRATCH_BYTES = 32 << 20
 LSTM_TRACE_MAX_STEPS = 512
 LSTM_TRACE_EVENTS = 16
@@ -48,12 +49,24 @@ class lstm_desc(ctypes.Structure):
                 ("dropout", ctypes.c_float), ("dropout_seed", ctypes.c_ulonglong)]
 
 
+class lstm_adamw_desc(ctypes.Structure):
+    _fields_ = [("num_tensors", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("seed", ctypes.c_ulonglong)]
+
+
 def make_desc(input_size, hidden_size, num_layers=1, bidirectional=False, bias=True,
               batch_first=True, batch=1, seq_len=1, dtype=LSTM_F32, dropout=0.0,
               dropout_seed=0) -> lstm_desc:
     return lstm_desc(int(input_size), int(hidden_size), int(num_layers), int(bool(bidirectional)),
                      int(bool(bias)), int(bool(batch_first)), int(batch), int(seq_len), int(dtype),
                      float(dropout), int(dropout_seed))
+
+
+def make_adamw_desc(num_tensors, grad_dtype=LSTM_F32, state_bits=32, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8,
+                    weight_decay=0.01, seed=0) -> lstm_adamw_desc:
+    return lstm_adamw_desc(int(num_tensors), int(grad_dtype), int(state_bits), float(lr), float(beta1),
+                           float(beta2), float(eps), float(weight_decay), int(seed))
 
 
 _lib = None
@@ -116,6 +129,12 @@ def load(build_if_stale: bool = True):
     lib.lstm_trace_enable.restype = ctypes.c_int
     lib.lstm_trace_read.argtypes = [ctypes.POINTER(ctypes.c_ulonglong), ctypes.c_int, ctypes.POINTER(ctypes.c_int)]
     lib.lstm_trace_read.restype = ctypes.c_int
+    ap = ctypes.POINTER(lstm_adamw_desc)
+    lp = ctypes.POINTER(ctypes.c_longlong)
+    lib.lstm_adamw_step.argtypes = [ap, lp] + [vpp] * 7 + [vp, vp, vp]
+    lib.lstm_adamw_step.restype = ctypes.c_int
+    lib.lstm_adamw_read_state.argtypes = [ap, lp] + [vpp] * 6 + [vp]
+    lib.lstm_adamw_read_state.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -245,6 +264,27 @@ def lstm_trace_read(max_steps: int = LSTM_TRACE_MAX_STEPS):
         raise LstmError(LSTM_ERR_CUDA, "lstm_trace_read")
     rows = [list(buf[i * LSTM_TRACE_EVENTS:(i + 1) * LSTM_TRACE_EVENTS]) for i in range(n)]
     return int(kind.value), rows
+
+
+def _numels(ts):
+    return (ctypes.c_longlong * len(ts))(*[int(t) for t in ts])
+
+
+def lstm_adamw_step(desc, numel, param, param_bf16, grad, m, v, m_scale, v_scale, step, scalars=None,
+                    stream=None) -> int:
+    """numel: ints; the other lists: tensors, device addresses or None entries (see optim.AdamW, which
+    keeps these arrays and checks the tensors).  Lists already made into ctypes arrays pass as they are."""
+    a = [x if x is None or isinstance(x, ctypes.Array) else _parr(x)
+         for x in (param, param_bf16, grad, m, v, m_scale, v_scale)]
+    n = numel if isinstance(numel, ctypes.Array) else _numels(numel)
+    return load().lstm_adamw_step(ctypes.byref(desc), n, *a, _p(step), _p(scalars), _stream(stream))
+
+
+def lstm_adamw_read_state(desc, numel, m, v, m_scale, v_scale, m_out, v_out, stream=None) -> int:
+    a = [x if x is None or isinstance(x, ctypes.Array) else _parr(x)
+         for x in (m, v, m_scale, v_scale, m_out, v_out)]
+    n = numel if isinstance(numel, ctypes.Array) else _numels(numel)
+    return load().lstm_adamw_read_state(ctypes.byref(desc), n, *a, _stream(stream))
 
 
 def check(status: int, where: str = "lstm") -> None:

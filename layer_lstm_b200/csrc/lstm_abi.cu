@@ -21,6 +21,7 @@
 
 #include "../../include/lstm.h"
 #include "lstm_internal.h"
+#include "lstm_ops.h"
 
 namespace lstm {
 namespace {
@@ -93,12 +94,15 @@ uint64_t timeout_ns() {
 // CUDA cores.
 enum Kind {
     K_PACK = 0, K_PROJ_TC, K_PROJ_SIMT, K_FWD_REC_TC, K_FWD_REC_FFMA, K_BWD_REC_FFMA, K_DW_TC, K_DW_SIMT,
-    K_DX_TC, K_DX_SIMT, K_DB, K_COPY, K_TRANSPOSE, K_DROPOUT, K_BWD_REC_TC, K_COUNT
+    K_DX_TC, K_DX_SIMT, K_DB, K_COPY, K_TRANSPOSE, K_DROPOUT, K_BWD_REC_TC,
+    K_OPS,                            // the kinds of lstm_ops.h, in OpKind order
+    K_COUNT = K_OPS + kOpKinds
 };
 const char* const kKindNames[K_COUNT] = {"pack",       "proj_gemm_tc", "proj_gemm_simt", "fwd_rec_tc",
                                          "fwd_rec_ffma", "bwd_rec_ffma", "dw_gemm_tc",   "dw_gemm_simt",
                                          "dx_gemm_tc", "dx_gemm_simt", "db_reduce",    "seq_copy",
-                                         "transpose",  "dropout", "bwd_rec_tc"};
+                                         "transpose",  "dropout", "bwd_rec_tc",
+                                         "adamw"};
 
 // Dropout launch for boundary `layer` over n time-major elements.
 DropoutArgs dropout_args(const lstm_desc* d, int layer, const void* src, void* dst, DType dt, long long n) {
@@ -467,6 +471,12 @@ unsigned long long* trace_for(int kind, int steps, cudaStream_t s) {
     ts.kind = kind;
     ts.steps = std::min(steps, kTraceSteps);
     return static_cast<unsigned long long*>(p);
+}
+
+cudaError_t timed_op(OpKind kind, cudaStream_t s, cudaError_t (*launch)(const void*, cudaStream_t, int*),
+                     const void* args) {
+    int n = 1;
+    return timed(K_OPS + (int)kind, s, [&] { return launch(args, s, &n); }, &n);
 }
 
 }  // namespace lstm

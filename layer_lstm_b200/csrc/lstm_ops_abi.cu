@@ -1,0 +1,119 @@
+// C-ABI entry points of the operators beside the LSTM (include/lstm.h,
+// "Operators beside the LSTM"): argument checks on the host, then the
+// kernels' launchers under the library's kernel timing.
+#include <math.h>
+
+#include <mutex>
+#include <vector>
+
+#include "../../include/lstm.h"
+#include "lstm_ops.h"
+
+namespace lstm {
+namespace {
+
+// SMs of the current device (0 if it cannot be asked), looked up once each.
+int num_sms() {
+    static std::mutex mu;
+    static std::vector<int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if ((int)cache.size() <= dev) cache.resize(dev + 1, 0);
+    if (!cache[dev] && cudaDeviceGetAttribute(&cache[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        cache[dev] = 0;
+    return cache[dev];
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+// A required pointer to elements of `a` bytes.
+bool given(const void* p, size_t a) { return p && aligned(p, a); }
+bool finite_ge0(double x) { return isfinite(x) && x >= 0.0; }
+
+bool valid(const lstm_adamw_desc* d) {
+    return d && d->num_tensors >= 0 && (d->grad_dtype == LSTM_F32 || d->grad_dtype == LSTM_BF16) &&
+           (d->state_bits == 8 || d->state_bits == 32) && finite_ge0(d->lr) && d->beta1 >= 0.0 && d->beta1 < 1.0 &&
+           d->beta2 >= 0.0 && d->beta2 < 1.0 && finite_ge0(d->eps) && d->eps > 0.0 && finite_ge0(d->weight_decay);
+}
+
+}  // namespace
+}  // namespace lstm
+
+using namespace lstm;
+
+extern "C" {
+
+lstm_status lstm_adamw_step(const lstm_adamw_desc* desc, const long long* numel, float* const* param,
+                            void* const* param_bf16, const void* const* grad, void* const* m, void* const* v,
+                            float* const* m_scale, float* const* v_scale, long long* step,
+                            const float* scalars, cudaStream_t stream) {
+    if (!valid(desc) || !given(step, 8) || !aligned(scalars, 4)) return LSTM_ERR_INVALID_ARG;
+    const int N = desc->num_tensors;
+    const bool eight = desc->state_bits == 8;
+    if (N > 0 && (!numel || !param || !grad || !m || !v || (eight && (!m_scale || !v_scale))))
+        return LSTM_ERR_INVALID_ARG;
+    const size_t ge = desc->grad_dtype == LSTM_F32 ? 4 : 2, se = eight ? 1 : 4;
+    for (int i = 0; i < N; ++i) {
+        if (numel[i] < 0) return LSTM_ERR_INVALID_ARG;
+        if (numel[i] == 0) continue;
+        if (!given(param[i], 4) || !given(grad[i], ge) || !given(m[i], se) || !given(v[i], se))
+            return LSTM_ERR_INVALID_ARG;
+        if (eight && (!given(m_scale[i], 4) || !given(v_scale[i], 4))) return LSTM_ERR_INVALID_ARG;
+        if (param_bf16 && !aligned(param_bf16[i], 2)) return LSTM_ERR_INVALID_ARG;
+    }
+    AdamwArgs a{};
+    a.bits = desc->state_bits;
+    a.gdt = desc->grad_dtype == LSTM_F32 ? DType::F32 : DType::BF16;
+    a.lr = desc->lr; a.beta1 = desc->beta1; a.beta2 = desc->beta2; a.eps = desc->eps;
+    a.weight_decay = desc->weight_decay; a.seed = desc->seed;
+    a.step = step; a.scalars = scalars;
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return LSTM_ERR_CUDA;
+    for (int first = 0; first == 0 || first < N; first += kAdamwTensors) {
+        AdamwTensor t[kAdamwTensors];
+        a.count = N - first < kAdamwTensors ? N - first : kAdamwTensors;
+        a.first = first;
+        a.advance = first + a.count == N;
+        for (int i = 0; i < a.count; ++i) {
+            const int j = first + i;
+            t[i] = {param[j], param_bf16 ? param_bf16[j] : nullptr, grad[j], m[j], v[j],
+                    eight ? m_scale[j] : nullptr, eight ? v_scale[j] : nullptr, numel[j]};
+        }
+        a.t = t;
+        if (timed_op(OP_ADAMW, stream, launch_adamw, &a) != cudaSuccess) return LSTM_ERR_CUDA;
+    }
+    return LSTM_OK;
+}
+
+lstm_status lstm_adamw_read_state(const lstm_adamw_desc* desc, const long long* numel, void* const* m,
+                                  void* const* v, float* const* m_scale, float* const* v_scale,
+                                  float* const* m_out, float* const* v_out, cudaStream_t stream) {
+    if (!valid(desc) || desc->state_bits != 8) return LSTM_ERR_INVALID_ARG;
+    const int N = desc->num_tensors;
+    if (N > 0 && (!numel || !m || !v || !m_scale || !v_scale || !m_out || !v_out)) return LSTM_ERR_INVALID_ARG;
+    for (int i = 0; i < N; ++i) {
+        if (numel[i] < 0) return LSTM_ERR_INVALID_ARG;
+        if (numel[i] == 0) continue;
+        if (!m[i] || !v[i] || !given(m_scale[i], 4) || !given(v_scale[i], 4) || !given(m_out[i], 4) ||
+            !given(v_out[i], 4))
+            return LSTM_ERR_INVALID_ARG;
+    }
+    AdamwReadArgs a{};
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return LSTM_ERR_CUDA;
+    for (int first = 0; first < N; first += kAdamwTensors) {
+        AdamwTensor t[kAdamwTensors];
+        a.count = N - first < kAdamwTensors ? N - first : kAdamwTensors;
+        for (int i = 0; i < a.count; ++i) {
+            const int j = first + i;
+            t[i] = {nullptr, nullptr, nullptr, m[j], v[j], m_scale[j], v_scale[j], numel[j]};
+        }
+        a.t = t;
+        a.m_out = m_out + first;
+        a.v_out = v_out + first;
+        if (timed_op(OP_ADAMW, stream, launch_adamw_read, &a) != cudaSuccess) return LSTM_ERR_CUDA;
+    }
+    return LSTM_OK;
+}
+
+}  // extern "C"

@@ -81,10 +81,16 @@ class GradBucket:
             dst.copy_(src)
 
 
-def train_step(step, bucket: GradBucket, world: int, group=None) -> None:
+def train_step(step, bucket: GradBucket, world: int, group=None, optimizer=None) -> None:
     """One data-parallel training step: `step()` computes this rank's
-    gradients into the bucket, then (world > 1) one all-reduce sums them."""
+    gradients into the bucket, then (world > 1) one all-reduce sums them.
+    `optimizer` (optim.AdamW over the bucket's gradients, see
+    runner.DeviceProblem.optimizer) then updates the weights; every rank
+    starts from the same weights and sums the same gradients, so the ranks'
+    weights stay equal without an exchange of their own."""
     step()
     if world > 1:
         bucket.allreduce(group)
     bucket.finish()
+    if optimizer is not None:
+        optimizer.step()

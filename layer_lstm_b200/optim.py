@@ -1,0 +1,121 @@
+"""AdamW over the tensors of a model, on the library's multi-tensor kernel.
+
+`AdamW` holds the moments and the step counter on the GPU and keeps the
+pointer arrays that lstm_adamw_step takes, so a step costs one call.  The
+gradients are read from the tensors it was given (for a training problem:
+the gradient tensors the LSTM backward overwrites, or the views of a
+dp.GradBucket), the parameters are updated in place and, where the layers
+compute in bf16, written to their bf16 tensors too.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding
+
+BLOCK = 256   # elements of a tensor that share one scale of the 8-bit moments
+
+
+def _check(name, t, dtype, device, numel):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or t.numel() != numel \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of {numel} elements on {device}")
+
+
+class AdamW:
+    """params: float32 tensors; grads: as many float32 or bf16 tensors (one type) of the same sizes.
+
+    copies: bf16 tensors (or None entries) that receive the updated parameters.  state_bits: 32, or 8
+    (codes in blocks of 256 elements; see include/lstm.h).  scalars: float32 device tensor of two, the
+    factors of the learning rate and of the gradients, read at every step (a schedule or a loss scale
+    that a captured graph follows).  state: moments and step counter of an earlier run, a dict as
+    `state` of this class; they are used in place, not copied."""
+
+    def __init__(self, params, grads, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+                 copies=None, state_bits=32, seed=0, scalars=None, state=None):
+        self.params, self.grads = list(params), list(grads)
+        self.copies = list(copies) if copies is not None else None
+        n = len(self.params)
+        if len(self.grads) != n or (self.copies is not None and len(self.copies) != n):
+            raise ValueError("one gradient (and one copy) for each parameter")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        device = self.params[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        gdt = self.grads[0].dtype if n else torch.float32
+        if gdt not in (torch.float32, torch.bfloat16):
+            raise ValueError("gradients are float32 or bf16")
+        sizes = [p.numel() for p in self.params]
+        for i, k in enumerate(sizes):
+            _check(f"params[{i}]", self.params[i], torch.float32, device, k)
+            _check(f"grads[{i}]", self.grads[i], gdt, device, k)
+            if self.copies is not None and self.copies[i] is not None:
+                _check(f"copies[{i}]", self.copies[i], torch.bfloat16, device, k)
+        if scalars is not None:
+            _check("scalars", scalars, torch.float32, device, 2)
+        self.device, self.scalars = device, scalars
+        eight = state_bits == 8
+        if state is None:
+            mdt, vdt = (torch.int8, torch.uint8) if eight else (torch.float32, torch.float32)
+            state = dict(m=[torch.zeros(p.shape, device=device, dtype=mdt) for p in self.params],
+                         v=[torch.zeros(p.shape, device=device, dtype=vdt) for p in self.params],
+                         m_scale=None, v_scale=None, step=torch.zeros(1, device=device, dtype=torch.int64))
+            if eight:
+                for name in ("m_scale", "v_scale"):
+                    state[name] = [torch.zeros(-(-k // BLOCK), device=device) for k in sizes]
+        else:
+            for name, dt, div in (("m", torch.int8 if eight else torch.float32, 1),
+                                  ("v", torch.uint8 if eight else torch.float32, 1),
+                                  ("m_scale", torch.float32, BLOCK), ("v_scale", torch.float32, BLOCK)):
+                if div > 1 and not eight:
+                    continue
+                if len(state[name]) != n:
+                    raise ValueError(f"state: one {name} for each parameter")
+                for i, k in enumerate(sizes):
+                    _check(f"{name}[{i}]", state[name][i], dt, device, -(-k // div))
+            _check("step", state["step"], torch.int64, device, 1)
+        self.state = state
+        self.desc = binding.make_adamw_desc(
+            n, binding.LSTM_F32 if gdt == torch.float32 else binding.LSTM_BF16, state_bits, lr, beta1, beta2, eps,
+            weight_decay, seed)
+        self._numel = binding._numels(sizes)
+        self._ptr = {name: binding._parr(ts) for name, ts in
+                     (("param", self.params), ("copy", self.copies), ("grad", self.grads), ("m", state["m"]),
+                      ("v", state["v"]), ("m_scale", state.get("m_scale")), ("v_scale", state.get("v_scale")))}
+
+    def step(self, stream=None) -> None:
+        """One update of every tensor, on `stream` (default: the current stream of the tensors' device)."""
+        p = self._ptr
+        with torch.cuda.device(self.device):
+            st = binding.lstm_adamw_step(self.desc, self._numel, p["param"], p["copy"], p["grad"], p["m"], p["v"],
+                                         p["m_scale"], p["v_scale"], self.state["step"], self.scalars, stream)
+        binding.check(st, "lstm_adamw_step")
+
+    def read_state(self, m_out=None, v_out=None, stream=None):
+        """The moments as two flat float32 tensors, every parameter's after the one before."""
+        total = sum(p.numel() for p in self.params)
+        if m_out is None:
+            m_out = torch.empty(total, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(total, device=self.device)
+        for name, t in (("m_out", m_out), ("v_out", v_out)):
+            _check(name, t, torch.float32, self.device, total)
+        if self.desc.state_bits == 32:
+            with torch.cuda.device(self.device):
+                s = torch.cuda.current_stream() if stream is None else stream
+                s = torch.cuda.ExternalStream(s) if isinstance(s, int) else s
+                with torch.cuda.stream(s):
+                    for out, ts in ((m_out, self.state["m"]), (v_out, self.state["v"])):
+                        if ts:
+                            torch.cat([t.reshape(-1) for t in ts], out=out)
+            return m_out, v_out
+        outs, at = [[], []], 0
+        for p in self.params:
+            for k, t in enumerate((m_out, v_out)):
+                outs[k].append(t.data_ptr() + 4 * at)
+            at += p.numel()
+        p = self._ptr
+        with torch.cuda.device(self.device):
+            st = binding.lstm_adamw_read_state(self.desc, self._numel, p["m"], p["v"], p["m_scale"], p["v_scale"],
+                                               outs[0], outs[1], stream)
+        binding.check(st, "lstm_adamw_read_state")
+        return m_out, v_out

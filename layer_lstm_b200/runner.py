@@ -92,6 +92,17 @@ class DeviceProblem:
         if self.train:
             binding.check(self.backward(stream), "lstm_backward")
 
+    def optimizer(self, **kw):
+        """optim.AdamW over this problem's weights and biases and the gradients its backward writes
+        (make it after dp.GradBucket.adopt, which moves the gradients).  bf16 weights are updated
+        through float32 masters that the optimizer holds; the weights become their rounded copies."""
+        from .optim import AdamW
+        params = self.w_ih + self.w_hh + (self.b_ih + self.b_hh if self.wl.bias else [])
+        grads = self.dw_ih + self.dw_hh + (self.db_ih + self.db_hh if self.wl.bias else [])
+        if self.dt == torch.float32:
+            return AdamW(params, grads, **kw)
+        return AdamW([p.float() for p in params], grads, copies=params, **kw)
+
     def status(self, stream=None) -> int:
         return binding.lstm_query_status(self.workspace, stream)
 
