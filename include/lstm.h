@@ -251,6 +251,42 @@ lstm_status lstm_noalloc_query_status(cudaStream_t stream);
  */
 
 /*
+ * Layer normalisation of each row of a (rows, cols) array (Ba, Kiros and
+ * Hinton 2016), for instance the (B, T, D*H) output of a recurrent layer as
+ * B*T rows before the next layer reads it:
+ *   mean = sum(x) / cols,  var = sum((x - mean)^2) / cols,
+ *   rstd = 1 / sqrt(var + eps),  y = (x - mean) rstd weight + bias.
+ * x, y, weight, bias, grad_y and dx have the description's dtype; mean, rstd,
+ * dweight and dbias are float32, and so is all arithmetic (y and dx are
+ * rounded once).  weight and bias may be NULL (ones, zeros); mean and rstd
+ * may be NULL in the forward (inference).  Rows are contiguous.
+ * The backward, with xhat = (x - mean) rstd and g = grad_y weight:
+ *   dx = rstd (g - sum(g) / cols - xhat sum(g xhat) / cols),
+ *   dweight = sum over rows of grad_y xhat,  dbias = sum over rows of grad_y,
+ * reads the mean and rstd its forward wrote.  dx, dweight and dbias may each
+ * be NULL where not wanted; what is wanted is overwritten.  The sums over
+ * rows have a fixed order.  The workspace (256-byte aligned, size from the
+ * query) holds the row groups' sums and is needed for dweight or dbias only.
+ * y may be x and dx may be grad_y or x (in place); no other overlap.
+ */
+typedef struct {
+    long long rows;   /* >= 0; 0 gives dweight = dbias = 0 */
+    int cols;         /* >= 1 */
+    lstm_dtype dtype;
+    float eps;        /* >= 0, finite */
+} lstm_norm_desc;
+
+/* Workspace bytes of lstm_layer_norm_backward; 0 if the description is invalid. */
+size_t lstm_layer_norm_workspace_size(const lstm_norm_desc* desc);
+
+lstm_status lstm_layer_norm_forward(const lstm_norm_desc* desc, const void* x, const void* weight,
+                                    const void* bias, void* y, float* mean, float* rstd, cudaStream_t stream);
+lstm_status lstm_layer_norm_backward(const lstm_norm_desc* desc, const void* grad_y, const void* x,
+                                     const void* weight, const float* mean, const float* rstd, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                     cudaStream_t stream);
+
+/*
  * AdamW over all tensors of a model (Loshchilov and Hutter 2019).  With
  * t = *step + 1, g the gradient times scalars[1] and lr times scalars[0]
  * (factors 1 when scalars is NULL), per element in float32:
@@ -333,7 +369,7 @@ const char* lstm_status_string(lstm_status status);
  * engine: _tc tensor cores, _ffma / _simt CUDA cores): pack, proj_gemm_tc,
  * proj_gemm_simt, fwd_rec_tc, fwd_rec_ffma, bwd_rec_tc, bwd_rec_ffma,
  * dw_gemm_tc, dw_gemm_simt, dx_gemm_tc, dx_gemm_simt, db_reduce, seq_copy,
- * transpose, dropout, adamw.
+ * transpose, dropout, adamw, norm_fwd, norm_bwd.
  * lstm_timing_reset
  * zeroes the totals.  Process-wide and thread-safe; event recording adds a
  * few microseconds per launch, so leave it off outside measurements.

@@ -25,7 +25,8 @@ EXPORTED = ("lstm_workspace_size", "lstm_reserve_size", "lstm_forward", "lstm_ba
             "lstm_query_status", "lstm_status_string", "lstm_timing_enable", "lstm_timing_read",
             "lstm_timing_reset", "lstm_forward_noalloc", "lstm_trace_enable", "lstm_trace_read",
             "lstm_forward_varlen", "lstm_backward_varlen", "lstm_noalloc_query_status", "lstm_adamw_step",
-            "lstm_adamw_read_state")
+            "lstm_adamw_read_state", "lstm_layer_norm_workspace_size", "lstm_layer_norm_forward",
+            "lstm_layer_norm_backward")
 LSTM_NOALLOC_SCRATCH_BYTES = 32 << 20
 LSTM_TRACE_MAX_STEPS = 512
 LSTM_TRACE_EVENTS = 16
@@ -55,6 +56,11 @@ class lstm_adamw_desc(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("seed", ctypes.c_ulonglong)]
 
 
+class lstm_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 def make_desc(input_size, hidden_size, num_layers=1, bidirectional=False, bias=True,
               batch_first=True, batch=1, seq_len=1, dtype=LSTM_F32, dropout=0.0,
               dropout_seed=0) -> lstm_desc:
@@ -67,6 +73,10 @@ def make_adamw_desc(num_tensors, grad_dtype=LSTM_F32, state_bits=32, lr=1e-3, be
                     weight_decay=0.01, seed=0) -> lstm_adamw_desc:
     return lstm_adamw_desc(int(num_tensors), int(grad_dtype), int(state_bits), float(lr), float(beta1),
                            float(beta2), float(eps), float(weight_decay), int(seed))
+
+
+def make_norm_desc(rows, cols, dtype=LSTM_F32, eps=1e-5) -> lstm_norm_desc:
+    return lstm_norm_desc(int(rows), int(cols), int(dtype), float(eps))
 
 
 _lib = None
@@ -135,6 +145,13 @@ def load(build_if_stale: bool = True):
     lib.lstm_adamw_step.restype = ctypes.c_int
     lib.lstm_adamw_read_state.argtypes = [ap, lp] + [vpp] * 6 + [vp]
     lib.lstm_adamw_read_state.restype = ctypes.c_int
+    np_ = ctypes.POINTER(lstm_norm_desc)
+    lib.lstm_layer_norm_workspace_size.argtypes = [np_]
+    lib.lstm_layer_norm_workspace_size.restype = sz
+    lib.lstm_layer_norm_forward.argtypes = [np_] + [vp] * 7
+    lib.lstm_layer_norm_forward.restype = ctypes.c_int
+    lib.lstm_layer_norm_backward.argtypes = [np_] + [vp] * 9 + [sz, vp]
+    lib.lstm_layer_norm_backward.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -285,6 +302,74 @@ def lstm_adamw_read_state(desc, numel, m, v, m_scale, v_scale, m_out, v_out, str
          for x in (m, v, m_scale, v_scale, m_out, v_out)]
     n = numel if isinstance(numel, ctypes.Array) else _numels(numel)
     return load().lstm_adamw_read_state(ctypes.byref(desc), n, *a, _stream(stream))
+
+
+def _fits(t, numel, dtype, device):
+    """Whether `t` is what a call reads as `numel` contiguous elements of `dtype` on `device`: a tensor of
+    that kind, a plain device address, or None (an argument left out)."""
+    if t is None or isinstance(t, int):
+        return True
+    return t.numel() == numel and t.dtype == dtype and t.device == device and t.is_contiguous()
+
+
+def _torch_dtype(code):
+    import torch
+    return {LSTM_F32: torch.float32, LSTM_BF16: torch.bfloat16}.get(int(code))
+
+
+def _device(*ts):
+    """Device of the first tensor among the arguments; None when all are plain addresses."""
+    for t in ts:
+        if t is not None and not isinstance(t, int):
+            return t.device
+    return None
+
+
+def _call(device, stream, f):
+    """f(stream handle) with `device` current, so that a call on another device's tensors runs there, on
+    `stream` or that device's current stream.  A tensor that is not on a GPU is refused."""
+    if device is None:
+        return f(_stream(stream))
+    if device.type != "cuda":
+        return LSTM_ERR_INVALID_ARG
+    import torch
+    if device.index == torch.cuda.current_device():
+        return f(_stream(stream))
+    with torch.cuda.device(device):
+        return f(_stream(stream))
+
+
+def lstm_layer_norm_workspace_size(desc: lstm_norm_desc) -> int:
+    return int(load().lstm_layer_norm_workspace_size(ctypes.byref(desc)))
+
+
+def lstm_layer_norm_forward(desc, x, weight, bias, y, mean=None, rstd=None, stream=None) -> int:
+    """Tensors whose type, device, size or contiguity does not match the description are refused
+    (LSTM_ERR_INVALID_ARG); plain device addresses pass as they are."""
+    import torch
+    n, dt, dev = desc.rows * desc.cols, _torch_dtype(desc.dtype), _device(x, y)
+    if not (_fits(x, n, dt, dev) and _fits(y, n, dt, dev) and _fits(weight, desc.cols, dt, dev)
+            and _fits(bias, desc.cols, dt, dev) and _fits(mean, desc.rows, torch.float32, dev)
+            and _fits(rstd, desc.rows, torch.float32, dev)):
+        return LSTM_ERR_INVALID_ARG
+    lib = load()
+    return _call(dev, stream, lambda s: lib.lstm_layer_norm_forward(
+        ctypes.byref(desc), _p(x), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd), s))
+
+
+def lstm_layer_norm_backward(desc, grad_y, x, weight, mean, rstd, dx, dweight, dbias, workspace=None, stream=None,
+                             ws_bytes=None) -> int:
+    import torch
+    n, dt, dev, f32 = desc.rows * desc.cols, _torch_dtype(desc.dtype), _device(grad_y, x, dweight), torch.float32
+    if not (_fits(grad_y, n, dt, dev) and _fits(x, n, dt, dev) and _fits(dx, n, dt, dev)
+            and _fits(weight, desc.cols, dt, dev) and _fits(mean, desc.rows, f32, dev)
+            and _fits(rstd, desc.rows, f32, dev) and _fits(dweight, desc.cols, f32, dev)
+            and _fits(dbias, desc.cols, f32, dev) and _device(workspace) in (None, dev)):
+        return LSTM_ERR_INVALID_ARG
+    lib = load()
+    return _call(dev, stream, lambda s: lib.lstm_layer_norm_backward(
+        ctypes.byref(desc), _p(grad_y), _p(x), _p(weight), _p(mean), _p(rstd), _p(dx), _p(dweight), _p(dbias),
+        _p(workspace), _nbytes(workspace) if ws_bytes is None else ws_bytes, s))
 
 
 def check(status: int, where: str = "lstm") -> None:

@@ -10,7 +10,7 @@
 namespace lstm {
 
 // Timing kinds of these operators; names in lstm_abi.cu, same order.
-enum OpKind { OP_ADAMW = 0, kOpKinds };
+enum OpKind { OP_ADAMW = 0, OP_NORM_FWD, OP_NORM_BWD, kOpKinds };
 
 // Runs launch(args, s, &launches) bracketed by the library's kernel timing.
 cudaError_t timed_op(OpKind kind, cudaStream_t s, cudaError_t (*launch)(const void*, cudaStream_t, int*),
@@ -56,5 +56,32 @@ struct AdamwReadArgs {
     const AdamwTensor* t;
 };
 cudaError_t launch_adamw_read(const void* args, cudaStream_t s, int* nlaunch);
+
+// ---------------------------------------------------------------- layer norm
+struct NormFwdArgs {
+    long long rows;
+    int cols;
+    DType dt;
+    float eps;
+    const void* x; const void* w; const void* b;   // w, b: [cols] or null
+    void* y;
+    float* mean; float* rstd;                      // [rows] or null
+    int num_sms;
+};
+cudaError_t launch_norm_fwd(const void* args, cudaStream_t s, int* nlaunch);
+
+struct NormBwdArgs {
+    long long rows;
+    int cols;
+    DType dt;
+    const void* gy; const void* x; const void* w;
+    const float* mean; const float* rstd;
+    void* dx; float* dw; float* db;                // each may be null
+    float* part;                                   // [norm_partials][2][cols]
+    int num_sms;
+};
+// Row groups whose sums of dw and db are kept apart before they are added.
+int norm_partials(long long rows, int cols, int num_sms);
+cudaError_t launch_norm_bwd(const void* args, cudaStream_t s, int* nlaunch);
 
 }  // namespace lstm

@@ -36,6 +36,13 @@ bool valid(const lstm_adamw_desc* d) {
            d->beta2 >= 0.0 && d->beta2 < 1.0 && finite_ge0(d->eps) && d->eps > 0.0 && finite_ge0(d->weight_decay);
 }
 
+bool valid(const lstm_norm_desc* d) {
+    return d && d->rows >= 0 && d->cols >= 1 && (d->dtype == LSTM_F32 || d->dtype == LSTM_BF16) &&
+           isfinite(d->eps) && d->eps >= 0.0f;
+}
+
+DType dtype_of(lstm_dtype t) { return t == LSTM_F32 ? DType::F32 : DType::BF16; }
+
 }  // namespace
 }  // namespace lstm
 
@@ -63,7 +70,7 @@ lstm_status lstm_adamw_step(const lstm_adamw_desc* desc, const long long* numel,
     }
     AdamwArgs a{};
     a.bits = desc->state_bits;
-    a.gdt = desc->grad_dtype == LSTM_F32 ? DType::F32 : DType::BF16;
+    a.gdt = dtype_of(desc->grad_dtype);
     a.lr = desc->lr; a.beta1 = desc->beta1; a.beta2 = desc->beta2; a.eps = desc->eps;
     a.weight_decay = desc->weight_decay; a.seed = desc->seed;
     a.step = step; a.scalars = scalars;
@@ -114,6 +121,54 @@ lstm_status lstm_adamw_read_state(const lstm_adamw_desc* desc, const long long* 
         if (timed_op(OP_ADAMW, stream, launch_adamw_read, &a) != cudaSuccess) return LSTM_ERR_CUDA;
     }
     return LSTM_OK;
+}
+
+size_t lstm_layer_norm_workspace_size(const lstm_norm_desc* desc) {
+    if (!valid(desc)) return 0;
+    // the partition of the largest device this library runs on serves where no device is at hand
+    const int sms = num_sms();
+    const size_t n = (size_t)norm_partials(desc->rows, desc->cols, sms > 0 ? sms : 148);
+    return ((n > 0 ? n : 1) * 2 * (size_t)desc->cols * 4 + 255) / 256 * 256;
+}
+
+lstm_status lstm_layer_norm_forward(const lstm_norm_desc* desc, const void* x, const void* weight,
+                                    const void* bias, void* y, float* mean, float* rstd, cudaStream_t stream) {
+    if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
+    if (!aligned(weight, e) || !aligned(bias, e) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return LSTM_ERR_INVALID_ARG;
+    if (desc->rows > 0 && (!given(x, e) || !given(y, e))) return LSTM_ERR_INVALID_ARG;
+    if (desc->rows == 0) return LSTM_OK;
+    NormFwdArgs a{};
+    a.rows = desc->rows; a.cols = desc->cols; a.dt = dtype_of(desc->dtype); a.eps = desc->eps;
+    a.x = x; a.w = weight; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd;
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return LSTM_ERR_CUDA;
+    return timed_op(OP_NORM_FWD, stream, launch_norm_fwd, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+lstm_status lstm_layer_norm_backward(const lstm_norm_desc* desc, const void* grad_y, const void* x,
+                                     const void* weight, const float* mean, const float* rstd, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                                     cudaStream_t stream) {
+    if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
+    if (!aligned(weight, e) || !aligned(dx, e) || !aligned(dweight, 4) || !aligned(dbias, 4))
+        return LSTM_ERR_INVALID_ARG;
+    if (desc->rows > 0 && (!given(grad_y, e) || !given(x, e) || !given(mean, 4) || !given(rstd, 4)))
+        return LSTM_ERR_INVALID_ARG;
+    if (dweight || dbias) {
+        if (!given(workspace, 256)) return LSTM_ERR_INVALID_ARG;
+        if (ws_bytes < lstm_layer_norm_workspace_size(desc)) return LSTM_ERR_WORKSPACE;
+    }
+    if (!dx && !dweight && !dbias) return LSTM_OK;
+    NormBwdArgs a{};
+    a.rows = desc->rows; a.cols = desc->cols; a.dt = dtype_of(desc->dtype);
+    a.gy = grad_y; a.x = x; a.w = weight; a.mean = mean; a.rstd = rstd;
+    a.dx = dx; a.dw = dweight; a.db = dbias; a.part = static_cast<float*>(workspace);
+    a.num_sms = num_sms();
+    if (a.num_sms <= 0) return LSTM_ERR_CUDA;
+    return timed_op(OP_NORM_BWD, stream, launch_norm_bwd, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }
 
 }  // extern "C"
