@@ -251,6 +251,77 @@ lstm_status lstm_noalloc_query_status(cudaStream_t stream);
  */
 
 /*
+ * Linear attention with a decay for each head (Katharopoulos et al. 2020;
+ * Sun et al. 2023): a recurrence whose state is a key_size x value_size
+ * matrix per head,
+ *   S_t = g_h S_{t-1} + k_t^T v_t,   out_t = scale q_t S_t,
+ * with g_h = exp(log_decay[h]), log_decay <= 0 (values above 0 act as 0,
+ * below -1e4 as -1e4, which forgets at once).  Without the recurrence:
+ *   out_t = scale (sum_{j <= t} g^(t-j) (q_t . k_j) v_j + g^(t+1) q_t S_0),
+ * which is how a sequence is computed, in chunks.  The decay is a constant of
+ * the layer; no gradient is formed for it.
+ *   q, k (B, T, heads, key_size), v, out (B, T, heads, value_size), or
+ *     (T, B, ...) without batch_first, of the description's dtype;
+ *   ld_q, ld_k, ld_v: elements from one time row of q (k, v) to the next in
+ *     memory, at least heads * size, or 0 for rows without a gap; with them q,
+ *     k and v may be parts of one projection's output.  dq, dk, dv have the
+ *     same layouts; out and grad_out are contiguous;
+ *   s0, s_n, grad_sn, ds0 (B, heads, key_size, value_size) float32; s0 and
+ *     grad_sn may be NULL (zeros), s_n and ds0 NULL (not wanted); s_n may be
+ *     s0 (in place).
+ * lengths (device int32, per batch row, clamped to [0, seq_len]) or NULL, as
+ * in lstm_forward_varlen: out, dq, dk and dv are 0 at padded steps, s_n is
+ * the state after the row's last valid step (s0 for an empty row), what the
+ * inputs hold at padded steps is never read.
+ * The backward forms S again; it needs no reserve from the forward:
+ *   dS_t = scale q_t^T grad_out_t + g dS_{t+1} (+ grad_sn at the last step),
+ *   dq_t = scale grad_out_t S_t^T, dk_t = v_t dS_t^T, dv_t = k_t dS_t,
+ *   ds0 = g dS_1.
+ * dq, dk, dv are required and overwritten.
+ * Products are summed in float32 and the states are float32; out, dq, dk and
+ * dv are rounded once.  In bf16 the scores and the state are rounded to bf16
+ * as operands of the tensor cores where the key and value sizes allow them.
+ * A NaN or an infinity in a step's inputs may reach the outputs of earlier
+ * steps of the same chunk of up to 128.
+ * Sizes from 1 to 128 for key_size and value_size; larger ones return
+ * LSTM_ERR_UNSUPPORTED.  Workspace (256-byte aligned) from the query; it
+ * serves forward and backward.
+ */
+typedef struct {
+    int batch;        /* >= 0 */
+    int seq_len;      /* >= 0; 0 gives s_n = s0, ds0 = grad_sn */
+    int heads;        /* >= 1 */
+    int key_size;
+    int value_size;
+    int batch_first;  /* 1: (B, T, ...); 0: (T, B, ...) */
+    lstm_dtype dtype;
+    float scale;      /* finite */
+    long long ld_q;
+    long long ld_k;
+    long long ld_v;
+} lstm_attention_desc;
+
+/* Workspace bytes; 0 if the description is invalid or unsupported. */
+size_t lstm_linear_attention_workspace_size(const lstm_attention_desc* desc);
+
+lstm_status lstm_linear_attention_forward(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                          const void* k, const void* v, const float* log_decay, const float* s0,
+                                          void* out, float* s_n, void* workspace, size_t ws_bytes,
+                                          cudaStream_t stream);
+lstm_status lstm_linear_attention_backward(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                           const void* k, const void* v, const float* log_decay, const float* s0,
+                                           const void* grad_out, const float* grad_sn, void* dq, void* dk,
+                                           void* dv, float* ds0, void* workspace, size_t ws_bytes,
+                                           cudaStream_t stream);
+
+/* One step for every batch row (seq_len must be 1): reads q, k, v of one
+ * token per row, updates `state` in place and writes out = scale q S.  Rows
+ * whose length (lengths, or NULL) is below 1 keep their state and get out 0. */
+lstm_status lstm_linear_attention_step(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                       const void* k, const void* v, const float* log_decay, float* state,
+                                       void* out, cudaStream_t stream);
+
+/*
  * Layer normalisation of each row of a (rows, cols) array (Ba, Kiros and
  * Hinton 2016), for instance the (B, T, D*H) output of a recurrent layer as
  * B*T rows before the next layer reads it:
@@ -369,7 +440,7 @@ const char* lstm_status_string(lstm_status status);
  * engine: _tc tensor cores, _ffma / _simt CUDA cores): pack, proj_gemm_tc,
  * proj_gemm_simt, fwd_rec_tc, fwd_rec_ffma, bwd_rec_tc, bwd_rec_ffma,
  * dw_gemm_tc, dw_gemm_simt, dx_gemm_tc, dx_gemm_simt, db_reduce, seq_copy,
- * transpose, dropout, adamw, norm_fwd, norm_bwd.
+ * transpose, dropout, adamw, norm_fwd, norm_bwd, att_fwd, att_bwd, att_step.
  * lstm_timing_reset
  * zeroes the totals.  Process-wide and thread-safe; event recording adds a
  * few microseconds per launch, so leave it off outside measurements.

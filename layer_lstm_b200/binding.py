@@ -26,7 +26,8 @@ EXPORTED = ("lstm_workspace_size", "lstm_reserve_size", "lstm_forward", "lstm_ba
             "lstm_timing_reset", "lstm_forward_noalloc", "lstm_trace_enable", "lstm_trace_read",
             "lstm_forward_varlen", "lstm_backward_varlen", "lstm_noalloc_query_status", "lstm_adamw_step",
             "lstm_adamw_read_state", "lstm_layer_norm_workspace_size", "lstm_layer_norm_forward",
-            "lstm_layer_norm_backward")
+            "lstm_layer_norm_backward", "lstm_linear_attention_workspace_size", "lstm_linear_attention_forward",
+            "lstm_linear_attention_backward", "lstm_linear_attention_step")
 LSTM_NOALLOC_SCRATCH_BYTES = 32 << 20
 LSTM_TRACE_MAX_STEPS = 512
 LSTM_TRACE_EVENTS = 16
@@ -61,6 +62,13 @@ class lstm_norm_desc(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class lstm_attention_desc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("seq_len", ctypes.c_int), ("heads", ctypes.c_int),
+                ("key_size", ctypes.c_int), ("value_size", ctypes.c_int), ("batch_first", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("ld_q", ctypes.c_longlong),
+                ("ld_k", ctypes.c_longlong), ("ld_v", ctypes.c_longlong)]
+
+
 def make_desc(input_size, hidden_size, num_layers=1, bidirectional=False, bias=True,
               batch_first=True, batch=1, seq_len=1, dtype=LSTM_F32, dropout=0.0,
               dropout_seed=0) -> lstm_desc:
@@ -77,6 +85,15 @@ def make_adamw_desc(num_tensors, grad_dtype=LSTM_F32, state_bits=32, lr=1e-3, be
 
 def make_norm_desc(rows, cols, dtype=LSTM_F32, eps=1e-5) -> lstm_norm_desc:
     return lstm_norm_desc(int(rows), int(cols), int(dtype), float(eps))
+
+
+def make_attention_desc(batch, seq_len, heads, key_size, value_size, batch_first=True, dtype=LSTM_F32, scale=None,
+                        ld_q=0, ld_k=0, ld_v=0) -> lstm_attention_desc:
+    """scale: None for key_size ** -0.5; ld_*: elements between time rows, 0 for rows without a gap."""
+    return lstm_attention_desc(int(batch), int(seq_len), int(heads), int(key_size), int(value_size),
+                               int(bool(batch_first)), int(dtype),
+                               float(max(key_size, 1) ** -0.5 if scale is None else scale), int(ld_q), int(ld_k),
+                               int(ld_v))
 
 
 _lib = None
@@ -152,6 +169,15 @@ def load(build_if_stale: bool = True):
     lib.lstm_layer_norm_forward.restype = ctypes.c_int
     lib.lstm_layer_norm_backward.argtypes = [np_] + [vp] * 9 + [sz, vp]
     lib.lstm_layer_norm_backward.restype = ctypes.c_int
+    tp = ctypes.POINTER(lstm_attention_desc)
+    lib.lstm_linear_attention_workspace_size.argtypes = [tp]
+    lib.lstm_linear_attention_workspace_size.restype = sz
+    lib.lstm_linear_attention_forward.argtypes = [tp] + [vp] * 9 + [sz, vp]
+    lib.lstm_linear_attention_forward.restype = ctypes.c_int
+    lib.lstm_linear_attention_backward.argtypes = [tp] + [vp] * 13 + [sz, vp]
+    lib.lstm_linear_attention_backward.restype = ctypes.c_int
+    lib.lstm_linear_attention_step.argtypes = [tp] + [vp] * 8
+    lib.lstm_linear_attention_step.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -370,6 +396,75 @@ def lstm_layer_norm_backward(desc, grad_y, x, weight, mean, rstd, dx, dweight, d
     return _call(dev, stream, lambda s: lib.lstm_layer_norm_backward(
         ctypes.byref(desc), _p(grad_y), _p(x), _p(weight), _p(mean), _p(rstd), _p(dx), _p(dweight), _p(dbias),
         _p(workspace), _nbytes(workspace) if ws_bytes is None else ws_bytes, s))
+
+
+def lstm_linear_attention_workspace_size(desc: lstm_attention_desc) -> int:
+    return int(load().lstm_linear_attention_workspace_size(ctypes.byref(desc)))
+
+
+def _fits_rows(t, desc, size, ld, dtype, device):
+    """Whether `t` is an array of desc's time rows, heads and `size` elements, the rows `ld` apart (0: no
+    gap): an address, a tensor of four dimensions, or a contiguous one of another shape."""
+    if t is None or isinstance(t, int):
+        return True
+    if t.dtype != dtype or t.device != device or t.numel() != desc.batch * desc.seq_len * desc.heads * size:
+        return False
+    ld = ld or desc.heads * size
+    if t.numel() == 0 or (t.is_contiguous() and ld == desc.heads * size):
+        return True
+    if t.dim() != 4 or t.shape[2] != desc.heads or t.shape[3] != size:
+        return False
+    outer, inner, s = t.shape[0], t.shape[1], t.stride()
+    if (outer, inner) != ((desc.batch, desc.seq_len) if desc.batch_first else (desc.seq_len, desc.batch)):
+        return False
+    return ((size == 1 or s[3] == 1) and (desc.heads == 1 or s[2] == size) and (inner == 1 or s[1] == ld)
+            and (outer == 1 or s[0] == inner * ld))
+
+
+def _attention_fits(desc, dev, lengths, log_decay, qs, ks, vs, outs, states, workspace=None):
+    import torch
+    dt, f32 = _torch_dtype(desc.dtype), torch.float32
+    return (all(_fits_rows(t, desc, desc.key_size, desc.ld_q, dt, dev) for t in qs)
+            and all(_fits_rows(t, desc, desc.key_size, desc.ld_k, dt, dev) for t in ks)
+            and all(_fits_rows(t, desc, desc.value_size, desc.ld_v, dt, dev) for t in vs)
+            and all(_fits_rows(t, desc, desc.value_size, 0, dt, dev) for t in outs)
+            and all(_fits(t, desc.batch * desc.heads * desc.key_size * desc.value_size, f32, dev) for t in states)
+            and _fits(log_decay, desc.heads, f32, dev) and _fits(lengths, desc.batch, torch.int32, dev)
+            and _device(workspace) in (None, dev))
+
+
+def lstm_linear_attention_forward(desc, q, k, v, log_decay, s0, out, s_n, workspace, stream=None, ws_bytes=None,
+                                  lengths=None) -> int:
+    """Tensors that do not match the description (type, device, size, layout) are refused with
+    LSTM_ERR_INVALID_ARG; plain device addresses pass as they are."""
+    dev = _device(q, log_decay)
+    if not _attention_fits(desc, dev, lengths, log_decay, (q,), (k,), (v,), (out,), (s0, s_n), workspace):
+        return LSTM_ERR_INVALID_ARG
+    lib = load()
+    return _call(dev, stream, lambda s: lib.lstm_linear_attention_forward(
+        ctypes.byref(desc), _p(lengths), _p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(out), _p(s_n),
+        _p(workspace), _nbytes(workspace) if ws_bytes is None else ws_bytes, s))
+
+
+def lstm_linear_attention_backward(desc, q, k, v, log_decay, s0, grad_out, grad_sn, dq, dk, dv, ds0, workspace,
+                                   stream=None, ws_bytes=None, lengths=None) -> int:
+    dev = _device(q, log_decay)
+    if not _attention_fits(desc, dev, lengths, log_decay, (q, dq), (k, dk), (v, dv), (grad_out,),
+                           (s0, grad_sn, ds0), workspace):
+        return LSTM_ERR_INVALID_ARG
+    lib = load()
+    return _call(dev, stream, lambda s: lib.lstm_linear_attention_backward(
+        ctypes.byref(desc), _p(lengths), _p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(grad_out), _p(grad_sn),
+        _p(dq), _p(dk), _p(dv), _p(ds0), _p(workspace), _nbytes(workspace) if ws_bytes is None else ws_bytes, s))
+
+
+def lstm_linear_attention_step(desc, q, k, v, log_decay, state, out, stream=None, lengths=None) -> int:
+    dev = _device(q, log_decay)
+    if not _attention_fits(desc, dev, lengths, log_decay, (q,), (k,), (v,), (out,), (state,)):
+        return LSTM_ERR_INVALID_ARG
+    lib = load()
+    return _call(dev, stream, lambda s: lib.lstm_linear_attention_step(
+        ctypes.byref(desc), _p(lengths), _p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(out), s))
 
 
 def check(status: int, where: str = "lstm") -> None:

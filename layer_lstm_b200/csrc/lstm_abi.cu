@@ -102,7 +102,7 @@ const char* const kKindNames[K_COUNT] = {"pack",       "proj_gemm_tc", "proj_gem
                                          "fwd_rec_ffma", "bwd_rec_ffma", "dw_gemm_tc",   "dw_gemm_simt",
                                          "dx_gemm_tc", "dx_gemm_simt", "db_reduce",    "seq_copy",
                                          "transpose",  "dropout", "bwd_rec_tc",
-                                         "adamw", "norm_fwd", "norm_bwd"};
+                                         "adamw", "norm_fwd", "norm_bwd", "att_fwd", "att_bwd", "att_step"};
 
 // Dropout launch for boundary `layer` over n time-major elements.
 DropoutArgs dropout_args(const lstm_desc* d, int layer, const void* src, void* dst, DType dt, long long n) {

@@ -10,7 +10,7 @@
 namespace lstm {
 
 // Timing kinds of these operators; names in lstm_abi.cu, same order.
-enum OpKind { OP_ADAMW = 0, OP_NORM_FWD, OP_NORM_BWD, kOpKinds };
+enum OpKind { OP_ADAMW = 0, OP_NORM_FWD, OP_NORM_BWD, OP_ATT_FWD, OP_ATT_BWD, OP_ATT_STEP, kOpKinds };
 
 // Runs launch(args, s, &launches) bracketed by the library's kernel timing.
 cudaError_t timed_op(OpKind kind, cudaStream_t s, cudaError_t (*launch)(const void*, cudaStream_t, int*),
@@ -83,5 +83,57 @@ struct NormBwdArgs {
 // Row groups whose sums of dw and db are kept apart before they are added.
 int norm_partials(long long rows, int cols, int num_sms);
 cudaError_t launch_norm_bwd(const void* args, cudaStream_t s, int* nlaunch);
+
+// ---------------------------------------------------------------- linear attention
+// One product of the recurrence, for every (batch row, head):
+//   out_i = oscale (sum_{j <= i} bscale g^(i-j) (a_i . b_j) c_j + g^(i+e) a_i X0)
+// over the row's n valid steps, taken forwards (e = 1) or, with `reverse`,
+// backwards (e = 0), and the state after them
+//   X = g^n X0 + sum_j bscale g^(n-e-j) b_j^T c_j.
+// The forward is one such product; the backward is three (its gradients with
+// respect to q, k and v) on permuted operands.
+struct LinJob {
+    const void* a; long long lda;   // rows of da (a, b) and dc (c, o) elements per head, ld between time rows
+    const void* b; long long ldb;
+    const void* c; long long ldc;
+    void* o; long long ldo;
+    int da, dc;
+    int reverse;
+    float bscale, oscale;
+    const float* init;              // [B*H] X0, or null (zeros)
+    int init_t;                     // 1: X0 is stored transposed, [dc][da]
+    float* fin;                     // [B*H][da][dc] final state, or null
+};
+
+constexpr int kLinMaxDim = 128;
+constexpr int kLinChunk = 64;       // steps whose products form one score matrix
+
+struct LinArgs {
+    int B, T, H;
+    int batch_first;
+    DType dt;
+    const int* lengths;             // [B] or null
+    const float* log_decay;         // [H]
+    int njobs;
+    LinJob job[3];
+    int nseg, seg_len;              // the time axis in nseg parts of seg_len steps
+    float* buf;                     // nseg > 1: [njobs][B*H][nseg][da*dc] segment states
+};
+// Parts the time axis is cut into for njobs products; 1: none.
+int lin_segments(int B, int T, int H, int njobs, int num_sms, int* seg_len);
+cudaError_t launch_lin(const void* args, cudaStream_t s, int* nlaunch);
+
+struct LinStepArgs {
+    int B, H, dk, dv;
+    DType dt;
+    float scale;
+    const int* lengths;             // [B], rows with none are left alone; or null
+    const void* q; const void* k; const void* v;
+    long long ldq, ldk, ldv;        // elements between batch rows
+    const float* log_decay;
+    float* state;                   // [B][H][dk][dv], updated
+    void* out;
+};
+cudaError_t launch_lin_step(const void* args, cudaStream_t s, int* nlaunch);
 
 }  // namespace lstm

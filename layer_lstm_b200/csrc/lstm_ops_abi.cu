@@ -41,7 +41,45 @@ bool valid(const lstm_norm_desc* d) {
            isfinite(d->eps) && d->eps >= 0.0f;
 }
 
+bool valid(const lstm_attention_desc* d) {
+    if (!d || d->batch < 0 || d->seq_len < 0 || d->heads < 1 || d->key_size < 1 || d->value_size < 1) return false;
+    if (d->batch_first != 0 && d->batch_first != 1) return false;
+    if ((d->dtype != LSTM_F32 && d->dtype != LSTM_BF16) || !isfinite(d->scale)) return false;
+    const long long wk = (long long)d->heads * d->key_size, wv = (long long)d->heads * d->value_size;
+    // one work item per (row, head) of a product; 2^31 of them is more than a GPU holds
+    if ((long long)d->batch * d->heads > (1ll << 28)) return false;
+    return (d->ld_q == 0 || d->ld_q >= wk) && (d->ld_k == 0 || d->ld_k >= wk) && (d->ld_v == 0 || d->ld_v >= wv);
+}
+bool supported(const lstm_attention_desc* d) {
+    return d->key_size <= kLinMaxDim && d->value_size <= kLinMaxDim;
+}
+
 DType dtype_of(lstm_dtype t) { return t == LSTM_F32 ? DType::F32 : DType::BF16; }
+
+// Fields that every product of a description shares.
+LinArgs lin_args(const lstm_attention_desc* d, const int* lengths, const float* log_decay, int njobs, void* ws) {
+    LinArgs a{};
+    a.B = d->batch; a.T = d->seq_len; a.H = d->heads; a.batch_first = d->batch_first;
+    a.dt = dtype_of(d->dtype);
+    a.lengths = lengths; a.log_decay = log_decay;
+    a.njobs = njobs;
+    a.nseg = lin_segments(a.B, a.T, a.H, njobs, num_sms(), &a.seg_len);
+    a.buf = static_cast<float*>(ws);
+    return a;
+}
+
+size_t lin_ws(const lstm_attention_desc* d, int njobs) {
+    const int sms = num_sms();
+    int len = 0;
+    const int n = lin_segments(d->batch, d->seq_len, d->heads, njobs, sms > 0 ? sms : 148, &len);
+    return n <= 1 ? 0 : (size_t)njobs * d->batch * d->heads * n * d->key_size * d->value_size * 4;
+}
+
+struct Lds { long long q, k, v, o; };
+Lds lds_of(const lstm_attention_desc* d) {
+    const long long wk = (long long)d->heads * d->key_size, wv = (long long)d->heads * d->value_size;
+    return {d->ld_q ? d->ld_q : wk, d->ld_k ? d->ld_k : wk, d->ld_v ? d->ld_v : wv, wv};
+}
 
 }  // namespace
 }  // namespace lstm
@@ -169,6 +207,84 @@ lstm_status lstm_layer_norm_backward(const lstm_norm_desc* desc, const void* gra
     a.num_sms = num_sms();
     if (a.num_sms <= 0) return LSTM_ERR_CUDA;
     return timed_op(OP_NORM_BWD, stream, launch_norm_bwd, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+size_t lstm_linear_attention_workspace_size(const lstm_attention_desc* desc) {
+    if (!valid(desc) || !supported(desc)) return 0;
+    const size_t f = lin_ws(desc, 1), b = lin_ws(desc, 3), m = f > b ? f : b;
+    return (m + 255) / 256 * 256 + 256;
+}
+
+lstm_status lstm_linear_attention_forward(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                          const void* k, const void* v, const float* log_decay, const float* s0,
+                                          void* out, float* s_n, void* workspace, size_t ws_bytes,
+                                          cudaStream_t stream) {
+    if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    if (!supported(desc)) return LSTM_ERR_UNSUPPORTED;
+    const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
+    if (!given(log_decay, 4) || !aligned(lengths, 4) || !aligned(s0, 4) || !aligned(s_n, 4))
+        return LSTM_ERR_INVALID_ARG;
+    if (desc->batch > 0 && desc->seq_len > 0 && (!given(q, e) || !given(k, e) || !given(v, e) || !given(out, e)))
+        return LSTM_ERR_INVALID_ARG;
+    if (!given(workspace, 256)) return LSTM_ERR_INVALID_ARG;
+    if (ws_bytes < lstm_linear_attention_workspace_size(desc)) return LSTM_ERR_WORKSPACE;
+    if (desc->batch == 0) return LSTM_OK;
+    if (num_sms() <= 0) return LSTM_ERR_CUDA;
+    LinArgs a = lin_args(desc, lengths, log_decay, 1, workspace);
+    const Lds ld = lds_of(desc);
+    a.job[0] = {q, ld.q, k, ld.k, v, ld.v, out, ld.o, desc->key_size, desc->value_size, 0, 1.0f, desc->scale,
+                s0, 0, s_n};
+    return timed_op(OP_ATT_FWD, stream, launch_lin, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+lstm_status lstm_linear_attention_backward(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                           const void* k, const void* v, const float* log_decay, const float* s0,
+                                           const void* grad_out, const float* grad_sn, void* dq, void* dk,
+                                           void* dv, float* ds0, void* workspace, size_t ws_bytes,
+                                           cudaStream_t stream) {
+    if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    if (!supported(desc)) return LSTM_ERR_UNSUPPORTED;
+    const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
+    if (!given(log_decay, 4) || !aligned(lengths, 4) || !aligned(s0, 4) || !aligned(grad_sn, 4) || !aligned(ds0, 4))
+        return LSTM_ERR_INVALID_ARG;
+    if (desc->batch > 0 && desc->seq_len > 0 &&
+        (!given(q, e) || !given(k, e) || !given(v, e) || !given(grad_out, e) || !given(dq, e) || !given(dk, e) ||
+         !given(dv, e)))
+        return LSTM_ERR_INVALID_ARG;
+    if (!given(workspace, 256)) return LSTM_ERR_INVALID_ARG;
+    if (ws_bytes < lstm_linear_attention_workspace_size(desc)) return LSTM_ERR_WORKSPACE;
+    if (desc->batch == 0) return LSTM_OK;
+    if (num_sms() <= 0) return LSTM_ERR_CUDA;
+    LinArgs a = lin_args(desc, lengths, log_decay, 3, workspace);
+    const Lds ld = lds_of(desc);
+    const int dk_ = desc->key_size, dv_ = desc->value_size;
+    const float s = desc->scale;
+    // dq_i = s (sum_{j <= i} g^(i-j) (do_i . v_j) k_j + g^(i+1) do_i S0^T)
+    a.job[0] = {grad_out, ld.o, v, ld.v, k, ld.k, dq, ld.q, dv_, dk_, 0, 1.0f, s, s0, 1, nullptr};
+    // dk_j = sum_{i >= j} s g^(i-j) (v_j . do_i) q_i + g^(n-1-j) v_j dS_n^T
+    a.job[1] = {v, ld.v, grad_out, ld.o, q, ld.q, dk, ld.k, dv_, dk_, 1, s, 1.0f, grad_sn, 1, nullptr};
+    // dv_j = sum_{i >= j} s g^(i-j) (k_j . q_i) do_i + g^(n-1-j) k_j dS_n; its last state is ds0
+    a.job[2] = {k, ld.k, q, ld.q, grad_out, ld.o, dv, ld.v, dk_, dv_, 1, s, 1.0f, grad_sn, 0, ds0};
+    return timed_op(OP_ATT_BWD, stream, launch_lin, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
+}
+
+lstm_status lstm_linear_attention_step(const lstm_attention_desc* desc, const int* lengths, const void* q,
+                                       const void* k, const void* v, const float* log_decay, float* state,
+                                       void* out, cudaStream_t stream) {
+    if (!valid(desc) || desc->seq_len != 1) return LSTM_ERR_INVALID_ARG;
+    if (!supported(desc)) return LSTM_ERR_UNSUPPORTED;
+    const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
+    if (!given(log_decay, 4) || !aligned(lengths, 4)) return LSTM_ERR_INVALID_ARG;
+    if (desc->batch == 0) return LSTM_OK;
+    if (!given(q, e) || !given(k, e) || !given(v, e) || !given(out, e) || !given(state, 4))
+        return LSTM_ERR_INVALID_ARG;
+    const Lds ld = lds_of(desc);
+    LinStepArgs a{};
+    a.B = desc->batch; a.H = desc->heads; a.dk = desc->key_size; a.dv = desc->value_size;
+    a.dt = dtype_of(desc->dtype); a.scale = desc->scale; a.lengths = lengths;
+    a.q = q; a.k = k; a.v = v; a.ldq = ld.q; a.ldk = ld.k; a.ldv = ld.v;
+    a.log_decay = log_decay; a.state = state; a.out = out;
+    return timed_op(OP_ATT_STEP, stream, launch_lin_step, &a) == cudaSuccess ? LSTM_OK : LSTM_ERR_CUDA;
 }
 
 }  // extern "C"
