@@ -9,6 +9,8 @@ compute in bf16, written to their bf16 tensors too.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import binding
@@ -78,21 +80,25 @@ class AdamW:
             n, binding.LSTM_F32 if gdt == torch.float32 else binding.LSTM_BF16, state_bits, lr, beta1, beta2, eps,
             weight_decay, seed)
         self._numel = binding._numels(sizes)
-        self._ptr = {name: binding._parr(ts) for name, ts in
-                     (("param", self.params), ("copy", self.copies), ("grad", self.grads), ("m", state["m"]),
-                      ("v", state["v"]), ("m_scale", state.get("m_scale")), ("v_scale", state.get("v_scale")))}
+        self._at = [sum(sizes[:i]) for i in range(n)]   # where each tensor starts in the flat moments
+        # the pointer arrays of lstm_adamw_step, in its order
+        self._ptr = [binding._parr(ts) for ts in
+                     (self.params, self.copies, self.grads, state["m"], state["v"], state.get("m_scale"),
+                      state.get("v_scale"))]
 
     def step(self, stream=None) -> None:
         """One update of every tensor, on `stream` (default: the current stream of the tensors' device)."""
         p = self._ptr
-        with torch.cuda.device(self.device):
-            st = binding.lstm_adamw_step(self.desc, self._numel, p["param"], p["copy"], p["grad"], p["m"], p["v"],
-                                         p["m_scale"], p["v_scale"], self.state["step"], self.scalars, stream)
+        if self.device.index == torch.cuda.current_device():
+            st = binding.lstm_adamw_step(self.desc, self._numel, *p, self.state["step"], self.scalars, stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = binding.lstm_adamw_step(self.desc, self._numel, *p, self.state["step"], self.scalars, stream)
         binding.check(st, "lstm_adamw_step")
 
     def read_state(self, m_out=None, v_out=None, stream=None):
         """The moments as two flat float32 tensors, every parameter's after the one before."""
-        total = sum(p.numel() for p in self.params)
+        total = sum(self._numel)
         if m_out is None:
             m_out = torch.empty(total, device=self.device)
         if v_out is None:
@@ -108,14 +114,9 @@ class AdamW:
                         if ts:
                             torch.cat([t.reshape(-1) for t in ts], out=out)
             return m_out, v_out
-        outs, at = [[], []], 0
-        for p in self.params:
-            for k, t in enumerate((m_out, v_out)):
-                outs[k].append(t.data_ptr() + 4 * at)
-            at += p.numel()
-        p = self._ptr
+        outs = [(ctypes.c_void_p * len(self.params))(*[t.data_ptr() + 4 * at for at in self._at])
+                for t in (m_out, v_out)]
         with torch.cuda.device(self.device):
-            st = binding.lstm_adamw_read_state(self.desc, self._numel, p["m"], p["v"], p["m_scale"], p["v_scale"],
-                                               outs[0], outs[1], stream)
+            st = binding.lstm_adamw_read_state(self.desc, self._numel, *self._ptr[3:], *outs, stream)
         binding.check(st, "lstm_adamw_read_state")
         return m_out, v_out

@@ -114,7 +114,7 @@ def test_packed_rows_are_recognised():
     q = p[..., :H * dk].view(B, T, H, dk)
     k = p[..., H * dk:2 * H * dk].view(B, T, H, dk)
     v = p[..., 2 * H * dk:].view(B, T, H, dv)
-    cpu = p.device
+    cpu = -1   # a CPU tensor's device index
     for t, size, ld in ((q, dk, d.ld_q), (k, dk, d.ld_k), (v, dv, d.ld_v)):
         assert binding._fits_rows(t, d, size, ld, torch.float32, cpu)
         assert not binding._fits_rows(t, d, size, 0, torch.float32, cpu)
