@@ -623,7 +623,9 @@ def main():
     if world != args.gpus:
         sys.exit(f"bench.py: --gpus {args.gpus} but the launcher started {world} ranks")
     if args.rank_probe:
-        print(f"rank-probe {rank} of {world}", flush=True)
+        # one write: ranks share the pipe, and print's newline may be a write of its own
+        sys.stdout.write(f"rank-probe {rank} of {world}\n")
+        sys.stdout.flush()
         return
     if args.impl == "reference":
         run_reference(args)
