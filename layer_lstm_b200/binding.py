@@ -355,10 +355,10 @@ def _device(*ts):
 def _call(device, stream, f, *args):
     """f(*args, stream handle) with GPU `device` current, so that a call on another device's tensors runs
     there, on `stream` or that device's current stream.  Tensors that are not on a GPU are refused."""
+    if device is not None and device < 0:
+        return LSTM_ERR_INVALID_ARG
     if device is None or device == torch.cuda.current_device():
         return f(*args, _stream(stream))
-    if device < 0:
-        return LSTM_ERR_INVALID_ARG
     with torch.cuda.device(device):
         return f(*args, _stream(stream))
 

@@ -473,6 +473,8 @@ unsigned long long* trace_for(int kind, int steps, cudaStream_t s) {
     return static_cast<unsigned long long*>(p);
 }
 
+uint64_t wait_limit_ns() { return timeout_ns(); }
+
 cudaError_t timed_op(OpKind kind, cudaStream_t s, cudaError_t (*launch)(const void*, cudaStream_t, int*),
                      const void* args) {
     int n = 1;

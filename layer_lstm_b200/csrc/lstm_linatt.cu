@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kThreads) lin_kernel(const __grid_constant__ L
     float* sp = sx + D * P;
     float* gp = sp + C * PC;   // g^0 .. g^C
 
+    if (MODE != kLinSegments && blockIdx.x == 0 && threadIdx.x == 0) *g.status = kStatusOk;
     LinItem it;
     lin_item(g, MODE, blockIdx.x, it);
     const LinJob& J = g.job[it.job];
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
         for (int s = 0; s < g.nseg; ++s) {
             const float own = buf[(size_t)s * n + i];
             buf[(size_t)s * n + i] = x;
-            const int m = min(g.seg_len, max(0, len - s * g.seg_len));
+            const int m = lin_steps(g, len, s, J.reverse);
             x = fmaf(expf(ld * (float)m), x, own);
         }
         if (J.fin) J.fin[(size_t)bh * n + i] = x;
@@ -358,17 +359,20 @@ cudaError_t step_type(const LinStepArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int lin_segments(int B, int T, int H, int njobs, int num_sms, int* seg_len) {
-    // Enough blocks for two on every SM; a segment is at least four chunks,
-    // since its state is written, carried and read again.
+int lin_segments(int B, int T, int H, int njobs, int num_sms, bool tc, int* seg_len) {
+    // Where rows, heads and products leave SMs idle: two blocks for every SM
+    // (one of the tensor-core kernel's); a segment is at least four chunks
+    // (two), since its state is written, carried and read again.
     const long long have = (long long)B * H * njobs;
-    const int chunks = (T + C - 1) / C;
+    const int chunk = tc ? kLinTcChunk : C, least = tc ? 2 : 4;
+    const long long want = tc ? num_sms : 2ll * num_sms;
+    const int chunks = (int)(((long long)T + chunk - 1) / chunk);
     int n = 1;
-    if (have > 0 && have * 2 <= 2ll * num_sms) n = (int)std::min<long long>((2ll * num_sms) / have, chunks / 4);
+    if (have > 0 && have * 2 <= want) n = (int)std::min<long long>(want / have, chunks / least);
     if (n < 1) n = 1;
-    const int per = (chunks + n - 1) / n;
-    *seg_len = std::max(1, per) * C;
-    return std::max(1, (T + *seg_len - 1) / *seg_len);
+    const int per = std::max(1, (chunks + n - 1) / n);
+    *seg_len = per * chunk;
+    return std::max(1, (chunks + per - 1) / per);
 }
 
 cudaError_t launch_lin_carry(const LinArgs& a, cudaStream_t s, int* n) {
@@ -379,8 +383,14 @@ cudaError_t launch_lin_carry(const LinArgs& a, cudaStream_t s, int* n) {
 }
 
 cudaError_t launch_lin(const void* args, cudaStream_t s, int* nlaunch) {
-    const LinArgs& a = *static_cast<const LinArgs*>(args);
+    LinArgs a = *static_cast<const LinArgs*>(args);
     *nlaunch = 0;
+    a.nseg = lin_segments(a.B, a.T, a.H, a.njobs, a.num_sms, true, &a.seg_len);
+    if (lin_tc_ok(a)) {
+        a.from_end = 1;
+        return launch_lin_tc(a, s, nlaunch);
+    }
+    a.nseg = lin_segments(a.B, a.T, a.H, a.njobs, a.num_sms, false, &a.seg_len);
     return a.dt == DType::F32 ? run_type<float>(a, s, nlaunch) : run_type<bf16>(a, s, nlaunch);
 }
 

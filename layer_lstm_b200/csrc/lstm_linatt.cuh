@@ -19,6 +19,14 @@ __device__ __forceinline__ int lin_length(const LinArgs& g, int b) {
     return g.lengths ? min(g.T, max(0, g.lengths[b])) : g.T;
 }
 
+// Valid steps of segment `seg` of a row of `len`.  The tensor-core kernel's
+// chunks end where the row ends, so forwards its first chunk is the short one.
+__device__ __forceinline__ int lin_steps(const LinArgs& g, int len, int seg, int reverse) {
+    const int pad = g.from_end && !reverse ? (kLinTcChunk - len % kLinTcChunk) % kLinTcChunk : 0;
+    const int t0 = max(0, seg * g.seg_len - pad), t1 = (seg + 1) * g.seg_len - pad;
+    return max(0, min(t1, len) - t0);
+}
+
 // Where the steps of one batch row lie: step tau of the product's own order
 // is time row `at(tau)` of the arrays.
 struct LinRow {

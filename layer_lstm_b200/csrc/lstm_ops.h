@@ -107,6 +107,7 @@ struct LinJob {
 
 constexpr int kLinMaxDim = 128;
 constexpr int kLinChunk = 64;       // steps whose products form one score matrix
+constexpr int kLinTcChunk = 128;    // the same on the tensor cores
 
 struct LinArgs {
     int B, T, H;
@@ -118,10 +119,23 @@ struct LinArgs {
     LinJob job[3];
     int nseg, seg_len;              // the time axis in nseg parts of seg_len steps
     float* buf;                     // nseg > 1: [njobs][B*H][nseg][da*dc] segment states
+    int from_end;                   // segments are counted from the valid steps' end (see lin_steps)
+    int* status;
+    uint64_t timeout_ns;
+    int num_sms;
 };
-// Parts the time axis is cut into for njobs products; 1: none.
-int lin_segments(int B, int T, int H, int njobs, int num_sms, int* seg_len);
+// Parts the time axis is cut into for njobs products; 1: none.  `tc`: for the
+// tensor-core kernel.
+int lin_segments(int B, int T, int H, int njobs, int num_sms, bool tc, int* seg_len);
 cudaError_t launch_lin(const void* args, cudaStream_t s, int* nlaunch);
+
+// The tensor-core kernel: whether these products can run on it (types, sizes,
+// alignment), and its launches.
+bool lin_tc_ok(const LinArgs& a);
+cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t s, int* n);
+
+// Limit of a bounded wait (lstm_query_status).
+uint64_t wait_limit_ns();
 
 struct LinStepArgs {
     int B, H, dk, dv;

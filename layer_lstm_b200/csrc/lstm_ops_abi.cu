@@ -63,15 +63,22 @@ LinArgs lin_args(const lstm_attention_desc* d, const int* lengths, const float* 
     a.dt = dtype_of(d->dtype);
     a.lengths = lengths; a.log_decay = log_decay;
     a.njobs = njobs;
-    a.nseg = lin_segments(a.B, a.T, a.H, njobs, num_sms(), &a.seg_len);
-    a.buf = static_cast<float*>(ws);
+    // the status word, as in every workspace, then the segments' states
+    a.status = static_cast<int*>(ws);
+    a.buf = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
+    a.timeout_ns = wait_limit_ns();
+    a.num_sms = num_sms();
     return a;
 }
 
 size_t lin_ws(const lstm_attention_desc* d, int njobs) {
     const int sms = num_sms();
-    int len = 0;
-    const int n = lin_segments(d->batch, d->seq_len, d->heads, njobs, sms > 0 ? sms : 148, &len);
+    int n = 1;
+    for (int tc = 0; tc < 2; ++tc) {   // which kernel runs depends on the pointers too
+        int len = 0;
+        const int k = lin_segments(d->batch, d->seq_len, d->heads, njobs, sms > 0 ? sms : 148, tc != 0, &len);
+        n = k > n ? k : n;
+    }
     return n <= 1 ? 0 : (size_t)njobs * d->batch * d->heads * n * d->key_size * d->value_size * 4;
 }
 
