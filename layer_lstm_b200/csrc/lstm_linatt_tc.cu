@@ -12,25 +12,29 @@
 // bf16 step.  X is
 // float32 and stays in its owners' registers during a walk: U is read from
 // tensor memory and added, and X's bf16 copy goes to shared memory as the next
-// chunk's operand.  The weighted values w c enter U's product split in two
-// bf16 parts (2^-16 of their size is lost), so the carried state is nearly
-// what float32 products give; the scores and the state enter the outputs'
-// products rounded once to bf16, as out itself is.  X is kept transposed, a
+// chunk's operand.  The weighted values w c enter U's product split in three
+// bf16 parts, which hold all of float32, so the carried state is what float32
+// products give; the scores and the state enter the outputs' products rounded
+// once to bf16, as out itself is.  X is kept transposed, a
 // thread per value column, so that states are read and written coalesced.
 //
 // Chunks end where the row's valid steps end, whatever the direction: the one
 // partial chunk lies before time 0, where TMA fills zeros, and padded steps
 // are never read.
 //
-// One block per SM walks (row, head, segment) items.  Warp 0 loads a, b, c by
-// TMA; warp 1 issues P, a X and P' c; warp 2 issues U; warps 3-6 (a thread per
-// step) turn P into P' and write out; warps 7-10 (a thread per value column)
-// weight c, and carry X.  Tensor memory: P (P' over it) | out | U | w c.
+// One block per SM walks (row, head, segment) items; its warps are stages of a
+// pipeline that runs across chunks and items, joined by mbarriers only:
+//   warp 0 loads a, b, c by TMA; warp 1 issues P, a X and P' c; warp 2 issues U;
+//   warps 4-7 (a thread per step) turn P into P' and write out;
+//   warps 8-11 (a thread per value column) weight c, 32 steps at a time;
+//   warps 12-15 (a thread per value column) carry X.
+// Tensor memory: P (P' over it; two of them for value sizes up to 64) | out | U
+// | w c (two sets of 32 steps).
 //
-// Bound: HBM (four rows of 2 d bytes a step).  A chunk's products are 2 to 4
-// million multiply-adds of 8192 a clock, an eighth of its load time; what has
-// to fit beside the loads are the two element passes, which is why they have
-// four warps each and no common barrier.
+// Bound: HBM (four rows of 2 d bytes a step).  A chunk's products take an
+// eighth of its load time on the tensor cores; what has to fit beside the
+// loads are the element passes, some 2000 issue slots of each of an SM's four
+// schedulers for 128 steps, and the hand-overs between them.
 #include <cuda.h>
 
 #include <algorithm>
@@ -44,8 +48,13 @@ namespace lstm {
 namespace {
 
 constexpr int kC = kLinTcChunk;        // steps a chunk
-constexpr int kThreadsTc = 352;
-constexpr int kTab = 400, kTabZero = 130;   // g^(n), n from -130 to 269
+constexpr int kThreadsTc = 512;
+// Registers a thread of each group of four warps (512 in all at launch): the
+// threads that carry X hold up to 128 sums.
+constexpr int kRegsControl = 96, kRegsOut = 128, kRegsWeight = 104, kRegsCarry = 184;
+static_assert(kRegsControl + kRegsOut + kRegsWeight + kRegsCarry <= 4 * 128, "registers of the block");
+constexpr int kSub = 32;               // steps weighted at a time
+constexpr int kTab = 260, kTabZero = 130;   // g^(n), n from -130 to 129
 
 struct Params {
     LinArgs g;
@@ -61,9 +70,10 @@ struct alignas(64) Maps {
     CUtensorMap m[4];
 };
 
-// HALF: value sizes (dc) up to 64.  The two bf16 parts of w c are then one
-// operand of 128 rows (lanes 0-63 the leading parts, 64-127 the remainders),
-// and X is kept as the two sums that gives.  DA: key sizes up to 64 or 128.
+// HALF: value sizes (dc) up to 64.  Operands of 128 rows then hold two of the
+// three bf16 parts of w c (lanes 0-63 the first, 64-127 the second; the third
+// in an operand of its own), and X is kept as the two sums that gives.  DA:
+// key sizes up to 64 or 128.
 template <bool HALF, int DA>
 struct Cfg {
     static constexpr int DCP = HALF ? 64 : 128;
@@ -72,10 +82,14 @@ struct Cfg {
     static constexpr int X_BYTES = DA * 256;
     static constexpr int S = HALF && DA == 64 ? 3 : 2;
     static constexpr int XB = HALF || DA == 64 ? 2 : 1;    // copies of X
-    static constexpr int TAB_BYTES = (2 * kC + kTab) * 4;
-    static constexpr int BARS = 2 * S + 6 + 2 * XB;
+    static constexpr int PB = HALF ? 2 : 1;                // scores in tensor memory
+    static constexpr int PARTS = HALF ? 2 : 3;             // operands that hold w c
+    static constexpr int TAB_BYTES = (2 * 3 * kC / 2 + kTab) * 4;
+    static constexpr int BARS = 2 * S + 8 + 2 * XB + 2 * PB;
     static constexpr size_t SMEM = (size_t)S * STAGE + XB * X_BYTES + TAB_BYTES + BARS * 8 + 16;
-    static constexpr int cP = 0, cO = 128, cU = 128 + DCP, cW = cU + DA;   // tensor-memory columns
+    // tensor-memory columns; a set of w c takes 16 of them for each operand
+    static constexpr int cP = 0, cO = PB * 128, cU = cO + DCP, cW = cU + DA;
+    static_assert(cW + 2 * PARTS * kSub / 2 <= 512, "tensor memory");
 };
 static_assert(Cfg<false, 128>::SMEM <= 232448, "shared memory of one block");
 
@@ -113,24 +127,105 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_half(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_half(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+// Four 8 x 8 matrices of 16-bit elements, transposed: lane t gets elements
+// (2 (t % 4), t / 4) and (2 (t % 4) + 1, t / 4) of each.
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 16 lanes x 16 columns of tensor memory from the registers of four such
+// matrices side by side: lane t holds rows t / 4 and t / 4 + 8, column t % 4
+// of each group of four.
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Two float32 products at once.
+__device__ __forceinline__ void mul2(float& a, float& b, unsigned long long f) {
+    unsigned long long x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(x), "l"(f));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Bounded wait, as tc::mbar_wait in few instructions: this kernel's warps run
+// six different programs on each scheduler and its speed hangs on how much of
+// them the instruction caches hold.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, const Params& p) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !tc::mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) == 0) {
+            if (*abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > p.timeout_ns) {
+                atomicCAS(p.status, kStatusOk, kStatusTimeout);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+// The chunks of a block's items, one after another.
+struct Chunks {
+    int item, c;
+    Walk w;
+    __device__ __forceinline__ Chunks() : item((int)blockIdx.x - (int)gridDim.x), c(0) { w.c1 = 0; }
+    // Moves to the next chunk; false at the end.
+    __device__ __forceinline__ bool next(const Params& p) {
+        ++c;
+        while (c >= w.c1) {
+            item += (int)gridDim.x;
+            if (item >= p.items) return false;
+            walk_of(p, item, w);
+            c = w.c0;
+        }
+        return true;
+    }
+};
+
 template <bool HALF, int DA>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     lin_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Cf = Cfg<HALF, DA>;
-    constexpr int S = Cf::S, XB = Cf::XB, DCP = Cf::DCP;
+    constexpr int S = Cf::S, XB = Cf::XB, PB = Cf::PB;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* sX = smem + S * Cf::STAGE;
-    float* sw = reinterpret_cast<float*>(sX + XB * Cf::X_BYTES);   // w_j: whole chunks, the reverse's partial one
-    float* sf = sw + 2 * kC;                                        // factors of P
+    // w of each pair of steps in three bf16 parts [2][3][kC / 2]: whole chunks,
+    // the reverse's partial one
+    uint32_t* sw = reinterpret_cast<uint32_t*>(sX + XB * Cf::X_BYTES);
+    float* sf = reinterpret_cast<float*>(sw + 2 * 3 * kC / 2);      // factors of P
     uint64_t* full = reinterpret_cast<uint64_t*>(sf + kTab);
     uint64_t* empty = full + S;
-    uint64_t* bP = empty + S;      // P computed
-    uint64_t* bPb = bP + 1;        // P' written
-    uint64_t* bO = bPb + 1;        // out computed
+    uint64_t* bP = empty + S;      // [PB] P computed
+    uint64_t* bPb = bP + PB;       // [PB] P' written
+    uint64_t* bO = bPb + PB;       // out computed
     uint64_t* bOf = bO + 1;        // out read
-    uint64_t* bW = bOf + 1;        // w c written
-    uint64_t* bU = bW + 1;         // U computed
-    uint64_t* bX = bU + 1;         // [XB] X written
+    uint64_t* bW = bOf + 1;        // [2] w c written
+    uint64_t* bWf = bW + 2;        // [2] w c read by the products
+    uint64_t* bU = bWf + 2;        // U computed
+    uint64_t* bUf = bU + 1;        // U read
+    uint64_t* bX = bUf + 1;        // [XB] X written
     uint64_t* bM2 = bX + XB;       // [XB] a X computed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bM2 + XB);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -138,16 +233,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool outs = p.mode != kLinStates;   // outputs wanted, not only states
     if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) tc::prefetch_tmap(&maps.m[i]);
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], outs ? 2 : 1);
         }
-        tc::mbar_init(bP, 1);
-        tc::mbar_init(bPb, 4);
+        for (int i = 0; i < PB; ++i) {
+            tc::mbar_init(&bP[i], 1);
+            tc::mbar_init(&bPb[i], 4);
+        }
         tc::mbar_init(bO, 1);
         tc::mbar_init(bOf, 4);
-        tc::mbar_init(bW, 4);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bW[i], 4);
+            tc::mbar_init(&bWf[i], 1);
+        }
         tc::mbar_init(bU, 1);
+        tc::mbar_init(bUf, 4);
         for (int i = 0; i < XB; ++i) {
             tc::mbar_init(&bX[i], 4);
             tc::mbar_init(&bM2[i], 1);
@@ -165,134 +267,150 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t* bar, int phase) {
-        return tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status, p.timeout_ns);
-    };
+    auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (uint32_t)(phase & 1), abort_flag, p); };
+    // descriptor of `d` moved by `bytes`
+    auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------- loads
-        if (lane == 0) {
-            int n = 0;
-            bool ok = true;
-            for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-                Walk w;
-                walk_of(p, item, w);
-                const LinJob& J = p.g.job[w.it.job];
-                const CUtensorMap* ma = &maps.m[p.map_a[w.it.job]];
-                const CUtensorMap* mb = &maps.m[p.map_b[w.it.job]];
-                const CUtensorMap* mc = &maps.m[p.map_c[w.it.job]];
-                const int na = (J.da + 63) / 64, nc = (J.dc + 63) / 64;
-                for (int c = w.c0; c < w.c1; ++c, ++n) {
+    if (warp < 4) {
+        regs_dec<kRegsControl>();
+        if (warp == 0) {
+            // --------------------------------------------------------- loads
+            if (lane == 0) {
+                int n = 0;
+                Chunks k;
+                for (; k.next(p); ++n) {
+                    const LinJob& J = p.g.job[k.w.it.job];
                     const int s = n % S;
-                    if (!wait(&empty[s], n / S + 1)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!wait(&empty[s], n / S + 1)) break;
+                    const CUtensorMap* ma = &maps.m[p.map_a[k.w.it.job]];
+                    const CUtensorMap* mb = &maps.m[p.map_b[k.w.it.job]];
+                    const CUtensorMap* mc = &maps.m[p.map_c[k.w.it.job]];
+                    const int na = (J.da + 63) / 64, nc = (J.dc + 63) / 64;
                     unsigned char* st = smem + s * Cf::STAGE;
                     tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((outs ? 2 : 1) * na + nc) * 16384));
-                    const int t = chunk_time(w, c, J.reverse);
-                    for (int k = 0; k < na; ++k) {
-                        const int x = w.it.h * J.da + 64 * k;
-                        tc::tma_load_3d(st + Cf::A_BYTES + k * 16384, mb, x, t, w.b, &full[s]);
-                        if (outs) tc::tma_load_3d(st + k * 16384, ma, x, t, w.b, &full[s]);
+                    const int t = chunk_time(k.w, k.c, J.reverse);
+                    for (int i = 0; i < na; ++i) {
+                        const int x = k.w.it.h * J.da + 64 * i;
+                        tc::tma_load_3d(st + Cf::A_BYTES + i * 16384, mb, x, t, k.w.b, &full[s]);
+                        if (outs) tc::tma_load_3d(st + i * 16384, ma, x, t, k.w.b, &full[s]);
                     }
-                    for (int k = 0; k < nc; ++k)
-                        tc::tma_load_3d(st + 2 * Cf::A_BYTES + k * 16384, mc, w.it.h * J.dc + 64 * k, t, w.b, &full[s]);
+                    for (int i = 0; i < nc; ++i)
+                        tc::tma_load_3d(st + 2 * Cf::A_BYTES + i * 16384, mc, k.w.it.h * J.dc + 64 * i, t, k.w.b, &full[s]);
+                }
+                if (*abort_flag) {   // copies in flight land before shared memory is released
+                    const uint64_t t0 = globaltimer_ns();
+                    for (int i = n > S ? n - S : 0; i < n; ++i)
+                        while (!tc::mbar_try_wait(&full[i % S], (uint32_t)((i / S) & 1)) &&
+                               globaltimer_ns() - t0 < 100000000ull) {}
                 }
             }
-            if (*abort_flag) {   // copies in flight land before shared memory is released
-                const uint64_t t0 = globaltimer_ns();
-                for (int k = n > S ? n - S : 0; k < n; ++k)
-                    while (!tc::mbar_try_wait(&full[k % S], (uint32_t)((k / S) & 1)) &&
-                           globaltimer_ns() - t0 < 100000000ull) {}
-            }
-        }
-    } else if (warp == 1) {
-        // --------------------------------------------- P, a X and P' c
-        int n = 0, last = -1;
-        bool ok = outs;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            Walk w;
-            walk_of(p, item, w);
-            const LinJob& J = p.g.job[w.it.job];
-            const int ka = J.da / 16;
-            const uint32_t idP = tc::instr_desc(1, 128, 128), idX = tc::instr_desc(1, 128, J.dc), idO = idX | (1u << 16);
-            for (int c = w.c0; c < w.c1; ++c, ++n) {
-                const int s = n % S;
-                const uint32_t sa = tc::smem_u32(smem + s * Cf::STAGE), sb = sa + Cf::A_BYTES, sc = sb + Cf::A_BYTES;
-                const uint32_t sx = tc::smem_u32(sX + (n % XB) * Cf::X_BYTES);
-                // P lies over the P' that the last chunk's product reads
-                if (!wait(&full[s], n / S) || (n > 0 && !wait(bO, n - 1))) { ok = false; break; }
+        } else if (warp == 1 && outs) {
+            // ----------------------------------------- P, a X and P' c
+            int n = 0;          // chunk of a X and P' c
+            int np = 0;         // chunk of P
+            Chunks k, kp;
+            // P of chunk np; it lies over the P' of PB chunks before
+            auto scores = [&]() {
+                if (!kp.next(p)) return true;
+                if (!wait(&full[np % S], np / S)) return false;
+                if (np >= PB && PB == 1 && !wait(bO, np - 1)) return false;
                 tc::tc_fence_after();
+                const int ka = p.g.job[kp.w.it.job].da / 16;
+                const uint64_t da = tc::smem_desc_sw128(tc::smem_u32(smem + (np % S) * Cf::STAGE));
+                const uint64_t db = at(da, Cf::A_BYTES);
+                const uint32_t id = tc::instr_desc(1, 128, 128), d = tmem + Cf::cP + (np % PB) * 128;
                 if (tc::elect_one()) {
-                    for (int k = 0; k < ka; ++k) {
-                        const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        tc::mma_bf16(tmem + Cf::cP, tc::smem_desc_sw128(sa + off), tc::smem_desc_sw128(sb + off), idP, k != 0);
+#pragma unroll 2
+                    for (int i = 0; i < ka; ++i) {
+                        const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
+                        tc::mma_bf16(d, at(da, off), at(db, off), id, i != 0);
                     }
-                    tc::mma_commit(bP);
+                    tc::mma_commit(&bP[np % PB]);
                 }
                 __syncwarp();
-                last = n;
-                if (!wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) { ok = false; break; }
+                ++np;
+                return true;
+            };
+            bool ok = scores();
+            for (; ok && k.next(p); ++n) {
+                const LinJob& J = p.g.job[k.w.it.job];
+                const int s = n % S, ka = J.da / 16;
+                const uint32_t sa = tc::smem_u32(smem + s * Cf::STAGE);
+                const uint64_t da = tc::smem_desc_sw128(sa);
+                const uint64_t dc = tc::smem_desc_sw128_mn(sa + 2 * Cf::A_BYTES, 16384);
+                const uint64_t dx = tc::smem_desc_sw128(tc::smem_u32(sX + (n % XB) * Cf::X_BYTES));
+                const uint32_t idX = tc::instr_desc(1, 128, J.dc), idO = idX | (1u << 16);
+                if (!wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
+#pragma unroll 1
                     for (int h = 0; h < (HALF ? 2 : 1); ++h)
-                        for (int k = 0; k < ka; ++k) {
-                            const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                            tc::mma_bf16(tmem + Cf::cO, tc::smem_desc_sw128(sa + off),
-                                         tc::smem_desc_sw128(sx + (uint32_t)(h * 8192) + off), idX, (h | k) != 0);
+#pragma unroll 2
+                        for (int i = 0; i < ka; ++i) {
+                            const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
+                            tc::mma_bf16(tmem + Cf::cO, at(da, off), at(dx, off + h * 8192), idX, (h | i) != 0);
                         }
                     tc::mma_commit(&bM2[n % XB]);
                 }
                 __syncwarp();
-                if (!wait(bPb, n)) { ok = false; break; }
+                // with two score buffers the next chunk's product runs beside this chunk's P'
+                if (PB == 2 && !scores()) break;
+                if (!wait(&bPb[n % PB], n / PB)) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
-                    for (int k = 0; k < kC / 16; ++k)
-                        tc::mma_bf16_ts(tmem + Cf::cO, tmem + Cf::cP + 8 * k,
-                                        tc::smem_desc_sw128_mn(sc + (uint32_t)(k * 2048), 16384), idO, 1);
+#pragma unroll 2
+                    for (int i = 0; i < kC / 16; ++i)
+                        tc::mma_bf16_ts(tmem + Cf::cO, tmem + Cf::cP + (n % PB) * 128 + 8 * i, at(dc, i * 2048), idO, 1);
                     tc::mma_commit(bO);
                     tc::mma_commit(&empty[s]);
                 }
                 __syncwarp();
+                if (PB == 1 && !scores()) break;
             }
-        }
-        if (*abort_flag && last >= 0) {   // products in flight end before tensor memory is released
-            if (tc::elect_one()) tc::mma_commit(&empty[last % S]);
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 1000000ull) {}
-        }
-    } else if (warp == 2) {
-        // ---------------------------------------------------------------- U
-        int n = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            Walk w;
-            walk_of(p, item, w);
-            const uint32_t id = tc::instr_desc(1, 128, p.g.job[w.it.job].da) | (1u << 16);
-            for (int c = w.c0; c < w.c1; ++c, ++n) {
+            if (*abort_flag) {   // products in flight end before tensor memory is released
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) {}
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ U
+            int n = 0;
+            Chunks k;
+            bool ok = true;
+            for (; ok && k.next(p); ++n) {
                 const int s = n % S;
-                const uint32_t sb = tc::smem_u32(smem + s * Cf::STAGE) + Cf::A_BYTES;
-                if (!wait(&full[s], n / S) || !wait(bW, n)) { ok = false; break; }
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
-                    for (int h = 0; h < (HALF ? 1 : 2); ++h)
-                        for (int k = 0; k < kC / 16; ++k)
-                            tc::mma_bf16_ts(tmem + Cf::cU, tmem + Cf::cW + h * 64 + 8 * k,
-                                            tc::smem_desc_sw128_mn(sb + (uint32_t)(k * 2048), 16384), id, (h | k) != 0);
-                    tc::mma_commit(bU);
-                    tc::mma_commit(&empty[s]);
+                const uint64_t db = tc::smem_desc_sw128_mn(tc::smem_u32(smem + s * Cf::STAGE) + Cf::A_BYTES, 16384);
+                const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.it.job].da) | (1u << 16);
+                if (!wait(&full[s], n / S) || (n > 0 && !wait(bUf, n - 1))) break;
+#pragma unroll 1
+                for (int r = 0; r < kC / kSub; ++r) {
+                    const int set = r & 1, turn = n * (kC / kSub / 2) + (r >> 1);
+                    if (!wait(&bW[set], turn)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int h = 0; h < Cf::PARTS; ++h)
+#pragma unroll
+                            for (int i = 0; i < kSub / 16; ++i)
+                                tc::mma_bf16_ts(tmem + Cf::cU, tmem + Cf::cW + (set * Cf::PARTS + h) * (kSub / 2) + 8 * i,
+                                                at(db, (uint32_t)(r * kSub + 16 * i) * 128), id, (r | h | i) != 0);
+                        tc::mma_commit(&bWf[set]);
+                        if (r == kC / kSub - 1) {
+                            tc::mma_commit(bU);
+                            tc::mma_commit(&empty[s]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            }
+            if (*abort_flag) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) {}
             }
         }
-        if (*abort_flag) {
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 1000000ull) {}
-        }
-    } else if (warp < 7) {
+    } else if (warp < 8) {
         // ------------------------------------------------ P -> P', out
-        const int q = warp & 3, i = q * 32 + lane, me = (warp - 3) * 32 + lane;
+        regs_dec<kRegsOut>();
+        const int q = warp & 3, i = q * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
         int n = 0;
         bool ok = outs;
@@ -310,22 +428,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc::named_bar_sync(1, 128);   // the last item's factors are read
             if (by_column) {
                 // g^(-tau_j - e): of the first chunk, then of the others
-                const int tj = rev ? kC - 1 - me : me;
-                sf[me] = expf(-ld * (float)(tj - first_pad + e)) * J.bscale;
-                sf[kC + me] = expf(-ld * (float)(tj + e)) * J.bscale;
+                const int tj = rev ? kC - 1 - i : i;
+                sf[i] = expf(-ld * (float)(tj - first_pad + e)) * J.bscale;
+                sf[kC + i] = expf(-ld * (float)(tj + e)) * J.bscale;
             } else {
-                for (int k = me; k < kTab; k += 128)
+                for (int k = i; k < kTab; k += 128)
                     sf[k] = expf(fminf(ld * (float)(k - kTabZero), 41.0f)) * J.bscale;
             }
             tc::named_bar_sync(1, 128);
-            bool good = true;
-            for (int c = w.c0; c < w.c1; ++c, ++n) {
-                const int pad = c == w.c0 ? first_pad : 0;
-                const int tau = rev ? kC - 1 - i : i - pad;
-                const int I = min(tau + e, cap);
-                if (!wait(bP, n)) { good = false; break; }
+            // the exponent of the step's state term
+            auto power = [&](int c) { return min(max(rev ? kC - 1 - i : i - (c == w.c0 ? first_pad : 0), 0) + e, cap); };
+
+            auto weigh = [&](int c, int nn) {   // P -> P' of chunk c
+                if (!wait(&bP[nn % PB], nn / PB)) return false;
                 tc::tc_fence_after();
+                const uint32_t tp = tl + Cf::cP + (nn % PB) * 128;
                 const float* fc = sf + (c == w.c0 ? 0 : kC);
+                const float* ft = sf + kTabZero - power(c);
 #pragma unroll 1
                 for (int kb = 0; kb < 4; ++kb) {
                     uint32_t r[16];
@@ -333,88 +452,108 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                         for (int k = 0; k < 16; ++k) r[k] = 0;
                     } else {
-                        float v[32];
-                        float v0[16], v1[16];
-                        tc::tmem_ld16(tl + Cf::cP + kb * 32, v0);
-                        tc::tmem_ld16(tl + Cf::cP + kb * 32 + 16, v1);
+                        float v[2][16];
+                        tc::tmem_ld16(tp + kb * 32, v[0]);
+                        tc::tmem_ld16(tp + kb * 32 + 16, v[1]);
                         tc::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) { v[k] = v0[k]; v[16 + k] = v1[k]; }
                         if (by_column) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(fc + kb * 32 + k);
-                                v[k] *= f.x; v[k + 1] *= f.y; v[k + 2] *= f.z; v[k + 3] *= f.w;
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fc + kb * 32 + k);
+                                float* x = &v[k >> 4][k & 15];
+                                mul2(x[0], x[1], f.x);
+                                mul2(x[2], x[3], f.y);
                             }
                         } else {
-                            // n = tau_i - tau_j - I(i)
-                            const float* ft = sf + kTabZero - I;
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 const int d = rev ? kb * 32 + k - i : i - kb * 32 - k;   // tau_i - tau_j
-                                v[k] = d >= 0 ? v[k] * ft[d] : 0.0f;
+                                float& x = v[k >> 4][k & 15];
+                                x = d >= 0 ? x * ft[d] : 0.0f;
                             }
                         }
                         if (kb == q) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (rev ? k < lane : k > lane) v[k] = 0.0f;
+                                if (rev ? k < lane : k > lane) v[k >> 4][k & 15] = 0.0f;
                         }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) r[k] = pack2(v[2 * k], v[2 * k + 1]);
+                        for (int k = 0; k < 16; ++k) r[k] = pack2(v[k >> 3][(2 * k) & 15], v[k >> 3][(2 * k + 1) & 15]);
                     }
-                    tc::tmem_st16(tl + Cf::cP + kb * 16, r);
+                    tc::tmem_st16(tp + kb * 16, r);
                 }
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bPb);
-                const float f = expf(ld * (float)I) * J.oscale;
-                if (!wait(bO, n)) { good = false; break; }
-                tc::tc_fence_after();
+                if (lane == 0) tc::mbar_arrive(&bPb[nn % PB]);
+                return true;
+            };
+            auto write = [&](int c, int nn) {   // out of chunk c
+                const float f = expf(ld * (float)power(c)) * J.oscale;
                 const int t = chunk_time(w, c, rev) + i;
-                bf16* dst = o + w.it.row.padded(t) * J.ldo;
-#pragma unroll
-                for (int cb = 0; cb < DCP / 32; ++cb) {
-                    if (cb * 32 >= J.dc) break;
-                    float v[16], u[16];
-                    tc::tmem_ld16(tl + Cf::cO + cb * 32, v);
-                    tc::tmem_ld16(tl + Cf::cO + cb * 32 + 16, u);
+                uint4* dst = reinterpret_cast<uint4*>(o + w.it.row.padded(t) * J.ldo);
+                if (!wait(bO, nn)) return false;
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < J.dc; cb += 32) {
+                    float v[2][16];
+                    tc::tmem_ld16(tl + Cf::cO + cb, v[0]);
+                    tc::tmem_ld16(tl + Cf::cO + cb + 16, v[1]);
                     tc::tmem_ld_wait();
-                    if ((cb + 1) * 32 >= J.dc) {   // all of out is in registers
+                    if (cb + 32 >= J.dc) {   // all of out is in registers
                         tc::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(bOf);
                     }
-                    if (t >= 0) {
-                        uint4* d4 = reinterpret_cast<uint4*>(dst + cb * 32);
+                    if (t < 0) continue;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            d4[k] = make_uint4(pack2(v[8 * k] * f, v[8 * k + 1] * f), pack2(v[8 * k + 2] * f, v[8 * k + 3] * f),
-                                               pack2(v[8 * k + 4] * f, v[8 * k + 5] * f), pack2(v[8 * k + 6] * f, v[8 * k + 7] * f));
-                        if (cb * 32 + 16 < J.dc) {
+                    for (int b = 0; b < 2; ++b) {
+                        if (cb + b * 16 >= J.dc) break;
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                d4[2 + k] = make_uint4(pack2(u[8 * k] * f, u[8 * k + 1] * f), pack2(u[8 * k + 2] * f, u[8 * k + 3] * f),
-                                                       pack2(u[8 * k + 4] * f, u[8 * k + 5] * f), pack2(u[8 * k + 6] * f, u[8 * k + 7] * f));
+                        for (int k = 0; k < 16; k += 8) {
+                            const float* x = &v[b][k];
+                            dst[(cb + b * 16 + k) / 8] = make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f),
+                                                                    pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
                         }
                     }
                 }
+                return true;
+            };
+            bool good = true;
+            for (int c = w.c0; c < w.c1 && good; ++c, ++n) {
+                good = weigh(c, n);
+                // with two score buffers out of the chunk before is written while P' c is computed
+                if (PB == 2) good = good && (c == w.c0 || write(c - 1, n - 1));
+                else good = good && write(c, n);
             }
+            if (PB == 2 && good && w.c0 < w.c1) good = write(w.c1 - 1, n - 1);
             // padded steps
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const int per = J.dc / 8;
-            for (int k = me; k < (w.it.pad1 - w.it.pad0) * per; k += 128)
+            for (int k = i; k < (w.it.pad1 - w.it.pad0) * per; k += 128)
                 *reinterpret_cast<uint4*>(o + w.it.row.padded(w.it.pad0 + k / per) * J.ldo + (k % per) * 8) = zero;
             // the four warps leave together
             if (tc::named_bar_or(1, 128, !good)) ok = false;
         }
-    } else {
-        // ------------------------------------------------ w c, X
-        const int q = warp & 3, l = q * 32 + lane, me = (warp - 7) * 32 + lane;
-        const int r = HALF ? (l & 63) : l;          // value column
-        const bool low = HALF && l >= 64;           // the remainders' half
-        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    } else if (warp < 12) {
+        // ------------------------------------------------ w c
+        // A pair of steps at a time in packed bf16, without leaving it: with
+        // w = w0 + w1 + w2 in three bf16 parts,
+        //   p0 = rn(c w0), e = c w0 - p0 (exact: the product has 16 bits),
+        //   p1 = rn(e + c w1), p2 = rn(c w2 + rn(c w1 + rn(e - p1))),
+        // six instructions for two elements, where going through float32
+        // takes seventeen.  ldmatrix turns the tile's rows (steps) into pairs
+        // of steps of one column, as the 16-lane store to tensor memory wants
+        // them.
+        regs_dec<kRegsWeight>();
+        const int q = warp & 3, l = q * 32 + lane;
+        const bool second = HALF && q >= 2;         // the rows of the second parts
+        const int col = (HALF ? q & 1 : q) * 32;    // first value column of the warp
+        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + Cf::cW;
+        // this lane's row of ldmatrix: step `row` of 16, 16-byte unit `unit` of the row
+        const int row = ((lane >> 4) << 3) + (lane & 7), unit = ((col & 63) >> 3) + ((lane >> 3) & 1);
+        const uint32_t lm = tc::smem_u32(smem) + 2 * Cf::A_BYTES + (uint32_t)((col >> 6) * 16384 + row * 128);
+        const uint32_t u0 = (uint32_t)((unit ^ (row & 7)) << 4), u1 = (uint32_t)(((unit + 2) ^ (row & 7)) << 4);
         int n = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
@@ -422,35 +561,128 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             walk_of(p, item, w);
             const LinJob& J = p.g.job[w.it.job];
             const int e = w.it.e, rev = J.reverse;
-            const float ld = w.it.ld;
             // w_j of whole chunks and of the reverse's partial one (the
             // forward's partial chunk has zeros where it has no steps)
             tc::named_bar_sync(2, 128);   // the last item's are read
+            {
+                const int k = l >> 6, j = (l & 63) * 2;   // variant, pair
+                float f[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int x = rev ? (k ? kC - w.pad : kC) - (kC - 1 - me) : kC - e - me;
-                sw[k * kC + me] = x >= 0 ? expf(ld * (float)x) * J.bscale : 0.0f;
-            }
-            float X[DA];
+                for (int u = 0; u < 2; ++u) {
+                    const int x = rev ? (k ? kC - w.pad : kC) - (kC - 1 - j - u) : kC - e - j - u;
+                    f[u] = x >= 0 ? expf(w.it.ld * (float)x) * J.bscale : 0.0f;
+                }
 #pragma unroll
-            for (int k = 0; k < DA; ++k) X[k] = 0.0f;
-            if (w.it.init && !low && r < J.dc) {
-                if (w.it.init_t) {
-                    const float4* x0 = reinterpret_cast<const float4*>(w.it.init + (size_t)r * J.da);
-#pragma unroll
-                    for (int k = 0; k < DA; k += 4)
-                        if (k < J.da) {
-                            const float4 v = x0[k / 4];
-                            X[k] = v.x; X[k + 1] = v.y; X[k + 2] = v.z; X[k + 3] = v.w;
-                        }
-                } else {
-                    const float* x0 = w.it.init + r;
-#pragma unroll
-                    for (int k = 0; k < DA; ++k)
-                        if (k < J.da) X[k] = x0[(size_t)k * J.dc];
+                for (int u = 0; u < 3; ++u) {
+                    const uint32_t h = pack2(f[0], f[1]);
+                    sw[(k * 3 + u) * (kC / 2) + (l & 63)] = h;
+                    f[0] -= lo_half(h);
+                    f[1] -= hi_half(h);
                 }
             }
             tc::named_bar_sync(2, 128);
+            bool good = true;
+            for (int c = w.c0; c < w.c1 && good; ++c, ++n) {
+                const uint32_t* wj = sw + (rev && c == w.nct - 1 ? 3 * kC / 2 : 0) + (lane & 3);
+                const int s = n % S;
+                if (!wait(&full[s], n / S)) { good = false; break; }
+#pragma unroll 1
+                for (int b = 0; b < kC / kSub; ++b) {
+                    const int set = b & 1, turn = n * (kC / kSub / 2) + (b >> 1);
+                    const uint32_t src = lm + (uint32_t)(s * Cf::STAGE + b * kSub * 128);
+                    // [lane half][8 registers: columns of 8 steps, rows 0-7 and 8-15 of the half]
+                    uint32_t p0[2][8], p1[2][8], p2[2][8];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        ldmatrix_t(src + t * 2048 + u0, &p0[0][4 * t]);
+                        ldmatrix_t(src + t * 2048 + u1, &p0[1][4 * t]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __nv_bfloat162 w0 = as_bf2(wj[b * 16 + 4 * k]), w1 = as_bf2(wj[kC / 2 + b * 16 + 4 * k]),
+                                             w2 = as_bf2(wj[kC + b * 16 + 4 * k]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int u = 2 * k; u < 2 * k + 2; ++u) {
+                                const __nv_bfloat162 x = as_bf2(p0[h][u]);
+                                const __nv_bfloat162 a0 = __hmul2_rn(x, w0);
+                                const __nv_bfloat162 ex = __hfma2(x, w0, __hneg2(a0));
+                                const __nv_bfloat162 a1 = __hfma2(x, w1, ex);
+                                const __nv_bfloat162 a2 = __hfma2(x, w2, __hfma2(x, w1, __hsub2_rn(ex, a1)));
+                                p0[h][u] = as_u32(a0);
+                                p1[h][u] = as_u32(a1);
+                                p2[h][u] = as_u32(a2);
+                            }
+                    }
+                    if (turn > 0 && !wait(&bWf[set], turn - 1)) { good = false; break; }
+                    tc::tc_fence_after();
+                    const uint32_t d = tl + set * Cf::PARTS * (kSub / 2);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t dh = d + ((uint32_t)(h * 16) << 16);
+                        if constexpr (HALF) {
+                            if (second) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) { p0[h][k] = p1[h][k]; p2[h][k] = 0; }
+                            }
+                            tmem_st_rows(dh, p0[h]);
+                            tmem_st_rows(dh + 16, p2[h]);
+                        } else {
+                            tmem_st_rows(dh, p0[h]);
+                            tmem_st_rows(dh + 16, p1[h]);
+                            tmem_st_rows(dh + 32, p2[h]);
+                        }
+                    }
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bW[set]);
+                }
+            }
+            if (tc::named_bar_or(2, 128, !good)) ok = false;
+        }
+    } else {
+        // ------------------------------------------------ X
+        regs_inc<kRegsCarry>();
+        const int q = warp & 3, l = q * 32 + lane;
+        const int r = HALF ? (l & 63) : l;          // value column
+        const bool second = HALF && l >= 64;        // the second parts' sums
+        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + Cf::cU;
+        int n = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
+            Walk w;
+            walk_of(p, item, w);
+            const LinJob& J = p.g.job[w.it.job];
+            const float ld = w.it.ld;
+            float X[DA];
+            if (w.it.init && !second && r < J.dc) {
+#pragma unroll
+                for (int kb = 0; kb < DA; kb += 16) {
+                    if (kb < J.da) {
+                        if (w.it.init_t) {
+                            const float4* x0 = reinterpret_cast<const float4*>(w.it.init + (size_t)r * J.da + kb);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 v = x0[k];
+                                X[kb + 4 * k] = v.x; X[kb + 4 * k + 1] = v.y;
+                                X[kb + 4 * k + 2] = v.z; X[kb + 4 * k + 3] = v.w;
+                            }
+                        } else {
+                            const float* x0 = w.it.init + (size_t)kb * J.dc + r;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) X[kb + k] = x0[(size_t)k * J.dc];
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) X[kb + k] = 0.0f;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < DA; ++k) X[k] = 0.0f;
+            }
             // X's bf16 copy for chunk n: 128-byte rows of 64 keys, swizzled
             auto put_x = [&]() {
                 if (n >= XB && !wait(&bM2[n % XB], n / XB - 1)) return false;
@@ -468,58 +700,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             bool good = true;
             if (outs && w.c0 < w.c1) good = put_x();
             for (int c = w.c0; c < w.c1 && good; ++c) {
-                const int m = c == (rev ? w.nct - 1 : 0) ? kC - w.pad : kC;
-                const float* wj = sw + (rev && c == w.nct - 1 ? kC : 0);
-                const int s = n % S;
-                if (!wait(&full[s], n / S)) { good = false; break; }
-                const unsigned char* sc = smem + s * Cf::STAGE + 2 * Cf::A_BYTES + (r >> 6) * 16384 + (r & 7) * 2;
-                const int ch = (r & 63) >> 3;
-#pragma unroll 1
-                for (int jb = 0; jb < kC; jb += 32) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(wj + jb + k);
-                        float v[4];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            v[u] = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(
-                                                       sc + (jb + k + u) * 128 + ((ch ^ ((k + u) & 7)) << 4))
-                                                   << 16);
-                        v[0] *= f.x; v[1] *= f.y; v[2] *= f.z; v[3] *= f.w;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t h = pack2(v[2 * u], v[2 * u + 1]);
-                            hi[k / 2 + u] = h;
-                            lo[k / 2 + u] = pack2(v[2 * u] - lo_half(h), v[2 * u + 1] - hi_half(h));
-                        }
-                    }
-                    if constexpr (HALF) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) hi[k] = low ? lo[k] : hi[k];
-                        tc::tmem_st16(tl + Cf::cW + jb / 2, hi);
-                    } else {
-                        tc::tmem_st16(tl + Cf::cW + jb / 2, hi);
-                        tc::tmem_st16(tl + Cf::cW + 64 + jb / 2, lo);
-                    }
-                }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bW);
+                const int m = c == (J.reverse ? w.nct - 1 : 0) ? kC - w.pad : kC;
                 const float gm = expf(ld * (float)m);
                 if (!wait(bU, n)) { good = false; break; }
                 tc::tc_fence_after();
 #pragma unroll
-                for (int cb = 0; cb < DA / 16; ++cb) {
-                    if (cb * 16 >= J.da) break;
-                    float v[16];
-                    tc::tmem_ld16(tl + Cf::cU + cb * 16, v);
+                for (int kb = 0; kb < DA; kb += 32) {
+                    if (kb >= J.da) break;
+                    float v[16], u[16];
+                    tc::tmem_ld16(tl + kb, v);
+                    if (kb + 16 < J.da) tc::tmem_ld16(tl + kb + 16, u);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) X[cb * 16 + k] = fmaf(gm, X[cb * 16 + k], v[k]);
+                    for (int k = 0; k < 16; ++k) X[kb + k] = fmaf(gm, X[kb + k], v[k]);
+                    if (kb + 16 < J.da) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) X[kb + 16 + k] = fmaf(gm, X[kb + 16 + k], u[k]);
+                    }
                 }
                 tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bUf);
                 ++n;
                 if (outs && c + 1 < w.c1) good = put_x();   // the next chunk's
             }
@@ -531,26 +732,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (outs)
                         for (int k = 1; k <= XB; ++k)
                             if (n - k >= 0 && good) good = wait(&bM2[(n - k) % XB], (n - k) / XB);
-                    if (low) {
+                    if (second) {
 #pragma unroll
                         for (int k = 0; k < DA; ++k) x[k * 64 + r] = X[k];
                     }
-                    tc::named_bar_sync(2, 128);
-                    if (!low) {
+                    tc::named_bar_sync(3, 128);
+                    if (!second) {
 #pragma unroll
                         for (int k = 0; k < DA; ++k) X[k] += x[k * 64 + r];
                     }
-                    tc::named_bar_sync(2, 128);
+                    tc::named_bar_sync(3, 128);
                 }
-                if (!low && r < J.dc) {
+                if (!second && r < J.dc) {
                     float* f = w.it.fin + r;
 #pragma unroll
-                    for (int k = 0; k < DA; ++k)
-                        if (k < J.da) f[(size_t)k * J.dc] = X[k];
+                    for (int kb = 0; kb < DA; kb += 16)
+                        if (kb < J.da) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) f[(size_t)(kb + k) * J.dc] = X[kb + k];
+                        }
                 }
             }
-            // the four warps leave together
-            if (tc::named_bar_or(2, 128, !good)) ok = false;
+            if (tc::named_bar_or(3, 128, !good)) ok = false;
         }
     }
     tc::tc_fence_before();
