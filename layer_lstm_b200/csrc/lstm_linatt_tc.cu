@@ -12,7 +12,7 @@
 // bf16 step.  X is
 // float32 and stays in its owners' registers during a walk: U is read from
 // tensor memory and added, and X's bf16 copy goes to shared memory as the next
-// chunk's operand.  The weighted values w c enter U's product split in three
+// chunk's operand.  The weighted values w c enter U's product split in four
 // bf16 parts, which hold all of float32, so the carried state is what float32
 // products give; the scores and the state enter the outputs' products rounded
 // once to bf16, as out itself is.  X is kept transposed, a
@@ -24,8 +24,10 @@
 //
 // One block per SM walks (row, head, segment) items; its warps are stages of a
 // pipeline that runs across chunks and items, joined by mbarriers only:
-//   warp 0 loads a, b, c by TMA; warp 1 issues P, a X and P' c; warp 2 issues U;
-//   warps 4-7 (a thread per step) turn P into P' and write out;
+//   warp 0 loads a, b, c and stores out by TMA; warp 1 issues P and P' c, warp 2
+//   U, warp 3 a X;
+//   warps 4-7 (a thread per step) turn P into P' and out into bf16, in the place
+//   of a;
 //   warps 8-11 (a thread per value column) weight c, 32 steps at a time;
 //   warps 12-15 (a thread per value column) carry X.
 // Tensor memory: P (P' over it; two of them for value sizes up to 64) | out | U
@@ -59,6 +61,8 @@ constexpr int kTab = 260, kTabZero = 130;   // g^(n), n from -130 to 129
 struct Params {
     LinArgs g;
     int map_a[3], map_b[3], map_c[3];   // tensor map of each job's operands
+    int tma_out[3];                     // out goes through shared memory and TMA (see run_mode)
+    int nmaps;
     int items;
     int mode;
     int reset;                          // first launch of a call: the status word starts anew
@@ -68,11 +72,12 @@ struct Params {
 
 struct alignas(64) Maps {
     CUtensorMap m[4];
+    CUtensorMap o[3];   // the jobs' outputs
 };
 
-// HALF: value sizes (dc) up to 64.  Operands of 128 rows then hold two of the
-// three bf16 parts of w c (lanes 0-63 the first, 64-127 the second; the third
-// in an operand of its own), and X is kept as the two sums that gives.  DA:
+// HALF: value sizes (dc) up to 64.  An operand of 128 rows then holds two of
+// the four bf16 parts of w c (lanes 0-63 one, 64-127 the other), and X is kept
+// as the two sums that gives.  DA:
 // key sizes up to 64 or 128.
 template <bool HALF, int DA>
 struct Cfg {
@@ -83,10 +88,10 @@ struct Cfg {
     static constexpr int S = HALF && DA == 64 ? 3 : 2;
     static constexpr int XB = HALF || DA == 64 ? 2 : 1;    // copies of X
     static constexpr int PB = HALF ? 2 : 1;                // scores in tensor memory
-    static constexpr int PARTS = HALF ? 2 : 3;             // operands that hold w c
+    static constexpr int PARTS = HALF ? 2 : 4;             // operands that hold w c
     static constexpr int TAB_BYTES = (2 * 3 * kC / 2 + kTab) * 4;
-    static constexpr int BARS = 2 * S + 8 + 2 * XB + 2 * PB;
-    static constexpr size_t SMEM = (size_t)S * STAGE + XB * X_BYTES + TAB_BYTES + BARS * 8 + 16;
+    static constexpr int BARS = 3 * S + 8 + 2 * XB + 2 * PB;
+    static constexpr size_t SMEM = (size_t)S * STAGE + XB * X_BYTES + TAB_BYTES + BARS * 8 + 48;
     // tensor-memory columns; a set of w c takes 16 of them for each operand
     static constexpr int cP = 0, cO = PB * 128, cU = cO + DCP, cW = cU + DA;
     static_assert(cW + 2 * PARTS * kSub / 2 <= 512, "tensor memory");
@@ -96,23 +101,67 @@ static_assert(Cfg<false, 128>::SMEM <= 232448, "shared memory of one block");
 // The decay that the outputs are formed with.
 __device__ __forceinline__ float out_decay(float ld) { return ld < -40.0f ? -40.0f : ld; }
 
+// Where a block is in the list of items, ((job B + b) H + h) nseg + seg, as its
+// digits; the next item is gridDim.x further, added digit by digit (a division
+// per item and role would be a third of the kernel's code).
 struct Walk {
-    LinItem it;
+    int item, seg, h, b, job;
     int len, c0, c1, nct;   // chunks [c0, c1) of the row's nct
     int pad;                // steps by which nct chunks exceed len
-    int b;
-};
 
-__device__ __forceinline__ void walk_of(const Params& p, int item, Walk& w) {
-    lin_item(p.g, p.mode, (unsigned)item, w.it);
-    const unsigned bh = ((unsigned)item / (unsigned)p.g.nseg) % (unsigned)(p.g.B * p.g.H);
-    w.b = (int)(bh / (unsigned)p.g.H);
-    w.len = lin_length(p.g, w.b);
-    w.nct = (w.len + kC - 1) / kC;
-    w.pad = w.nct * kC - w.len;
-    const int seg = item % p.g.nseg, per = p.g.seg_len / kC;
-    w.c0 = min(seg * per, w.nct);
-    w.c1 = min(w.c0 + per, w.nct);
+    __device__ __forceinline__ explicit Walk(const int* digits) {
+        item = (int)blockIdx.x - (int)gridDim.x;
+        seg = digits[0]; h = digits[1]; b = digits[2]; job = digits[3];
+        c1 = 0;
+    }
+    // Moves to the block's next item; false at the end.  digits[4..7]: those of gridDim.x.
+    __device__ __forceinline__ bool next(const Params& p, const int* digits) {
+        if (item >= 0) {
+            seg += digits[4];
+            h += digits[5];
+            b += digits[6];
+            job += digits[7];
+            if (seg >= p.g.nseg) { seg -= p.g.nseg; ++h; }
+            if (h >= p.g.H) { h -= p.g.H; ++b; }
+            if (b >= p.g.B) { b -= p.g.B; ++job; }
+        }
+        item += (int)gridDim.x;
+        if (item >= p.items) return false;
+        len = lin_length(p.g, b);
+        nct = (len + kC - 1) / kC;
+        pad = nct * kC - len;
+        const int per = p.g.seg_len / kC;
+        c0 = min(seg * per, nct);
+        c1 = min(c0 + per, nct);
+        return true;
+    }
+};
+// Row of the arrays that holds batch row b at time t.
+__device__ __forceinline__ long long time_row(const Params& p, int b, int t) {
+    return p.g.batch_first ? (long long)b * p.g.T + t : (long long)t * p.g.B + b;
+}
+// An item's states: the first, from the caller or the segments' buffer, and
+// where the last goes.
+__device__ __forceinline__ void state_of(const Params& p, const Walk& w, const float*& init, bool& init_t, float*& fin) {
+    const LinJob& J = p.g.job[w.job];
+    const size_t bh = (size_t)w.b * p.g.H + w.h, n = (size_t)J.da * J.dc;
+    if (p.mode == kLinWhole) {
+        init = J.init ? J.init + bh * n : nullptr;
+        init_t = J.init_t != 0;
+        fin = J.fin ? J.fin + bh * n : nullptr;
+    } else {
+        float* own = p.g.buf + lin_buf_offset(p.g, w.job) + (bh * p.g.nseg + w.seg) * n;
+        init = p.mode == kLinStates ? nullptr : own;
+        init_t = false;
+        fin = p.mode == kLinStates ? own : nullptr;
+    }
+}
+// The digits of item `n`.
+__device__ __forceinline__ void digits_of(const Params& p, int n, int* d) {
+    d[0] = n % p.g.nseg; n /= p.g.nseg;
+    d[1] = n % p.g.H; n /= p.g.H;
+    d[2] = n % p.g.B;
+    d[3] = n / p.g.B;
 }
 
 // Time of a chunk's first row (negative in the partial chunk).
@@ -139,6 +188,11 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t* r) {
                  : "memory");
 }
 
+__device__ __forceinline__ void lds4(const uint32_t* p, uint32_t (&r)[4]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    r[0] = q.x; r[1] = q.y; r[2] = q.z; r[3] = q.w;
+}
+
 // 16 lanes x 16 columns of tensor memory from the registers of four such
 // matrices side by side: lane t holds rows t / 4 and t / 4 + 8, column t % 4
 // of each group of four.
@@ -147,6 +201,18 @@ __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+
+// Tile of shared memory to box {c0, c1, c2} of a tensor, in this thread's bulk group.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's stores have read shared memory / have ended.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Two float32 products at once.
 __device__ __forceinline__ void mul2(float& a, float& b, unsigned long long f) {
@@ -165,22 +231,22 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Bounded wait, as tc::mbar_wait in few instructions: this kernel's warps run
-// six different programs on each scheduler and its speed hangs on how much of
-// them the instruction caches hold.
+// Bounded wait, as tc::mbar_wait in fewer instructions: this kernel's warps run
+// seven programs on each scheduler, and its speed hangs on how much of them the
+// instruction caches hold.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, const Params& p) {
     uint64_t t0 = 0;
+    uint32_t i = 0;
 #pragma unroll 1
-    for (uint32_t i = 1; !tc::mbar_try_wait(bar, parity); ++i) {
-        if ((i & 255u) == 0) {
-            if (*abort) return false;
-            const uint64_t t = globaltimer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > p.timeout_ns) {
-                atomicCAS(p.status, kStatusOk, kStatusTimeout);
-                *abort = 1;
-                return false;
-            }
+    while (!tc::mbar_try_wait(bar, parity)) {
+        if ((++i & 255u) != 0) continue;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (*abort) return false;
+        if (t - t0 > p.timeout_ns) {
+            atomicCAS(p.status, kStatusOk, kStatusTimeout);
+            *abort = 1;
+            return false;
         }
     }
     return true;
@@ -188,16 +254,15 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 
 // The chunks of a block's items, one after another.
 struct Chunks {
-    int item, c;
+    int c;
     Walk w;
-    __device__ __forceinline__ Chunks() : item((int)blockIdx.x - (int)gridDim.x), c(0) { w.c1 = 0; }
+    __device__ __forceinline__ explicit Chunks(const int* digits) : c(0), w(digits) {}
     // Moves to the next chunk; false at the end.
-    __device__ __forceinline__ bool next(const Params& p) {
+    __device__ __forceinline__ bool next(const Params& p, const int* digits) {
         ++c;
+#pragma unroll 1
         while (c >= w.c1) {
-            item += (int)gridDim.x;
-            if (item >= p.items) return false;
-            walk_of(p, item, w);
+            if (!w.next(p, digits)) return false;
             c = w.c0;
         }
         return true;
@@ -217,7 +282,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     float* sf = reinterpret_cast<float*>(sw + 2 * 3 * kC / 2);      // factors of P
     uint64_t* full = reinterpret_cast<uint64_t*>(sf + kTab);
     uint64_t* empty = full + S;
-    uint64_t* bP = empty + S;      // [PB] P computed
+    uint64_t* bS = empty + S;      // [S] out written in the place of a
+    uint64_t* bP = bS + S;         // [PB] P computed
     uint64_t* bPb = bP + PB;       // [PB] P' written
     uint64_t* bO = bPb + PB;       // out computed
     uint64_t* bOf = bO + 1;        // out read
@@ -229,14 +295,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint64_t* bM2 = bX + XB;       // [XB] a X computed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bM2 + XB);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* digits = reinterpret_cast<int*>(tmem_slot + 2);   // [8]: the first item's, gridDim.x's
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool outs = p.mode != kLinStates;   // outputs wanted, not only states
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) tc::prefetch_tmap(&maps.m[i]);
+        for (int i = 0; i < p.nmaps; ++i) tc::prefetch_tmap(&maps.m[i]);
         for (int s = 0; s < S; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], outs ? 2 : 1);
+            tc::mbar_init(&bS[s], 4);
         }
         for (int i = 0; i < PB; ++i) {
             tc::mbar_init(&bP[i], 1);
@@ -255,6 +323,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc::mbar_init(&bM2[i], 1);
         }
         *abort_flag = 0;
+        digits_of(p, (int)blockIdx.x, digits);
+        digits_of(p, (int)gridDim.x, digits + 4);
         tc::fence_mbar_init();
         // a bounded wait elsewhere gives up no sooner than its limit after this
         if (p.reset && blockIdx.x == 0) *p.status = kStatusOk;
@@ -274,54 +344,94 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (warp < 4) {
         regs_dec<kRegsControl>();
         if (warp == 0) {
-            // --------------------------------------------------------- loads
+            // ------------------------------------------------- loads, stores
             if (lane == 0) {
                 int n = 0;
-                Chunks k;
-                for (; k.next(p); ++n) {
-                    const LinJob& J = p.g.job[k.w.it.job];
+                Chunks k(digits);
+                // where out of the chunk that holds a stage goes: job (-1:
+                // nowhere by TMA), columns, time, batch row
+                int oj[S], ox[S], ot[S], ob[S];
+#pragma unroll
+                for (int s = 0; s < S; ++s) oj[s] = -1;
+                auto store = [&](int s, int nn) {   // out of chunk nn
+                    if (!wait(&bS[s], nn / S)) return false;
+                    int j = -1, x = 0, t = 0, b = 0;
+#pragma unroll
+                    for (int i = 0; i < S; ++i)
+                        if (i == s) { j = oj[i]; x = ox[i]; t = ot[i]; b = ob[i]; }
+                    if (j >= 0) {
+                        const int nc = p.g.job[j].dc / 64;
+#pragma unroll 1
+                        for (int i = 0; i < nc; ++i)
+                            tma_store_3d(&maps.o[j], smem + s * Cf::STAGE + i * 16384, x + 64 * i, t, b);
+                        bulk_commit();
+                    }
+                    return true;
+                };
+                bool ok = true;
+                for (; k.next(p, digits); ++n) {
+                    const int jn = k.w.job, h = k.w.h;
+                    const LinJob& J = p.g.job[jn];
                     const int s = n % S;
-                    if (!wait(&empty[s], n / S + 1)) break;
-                    const CUtensorMap* ma = &maps.m[p.map_a[k.w.it.job]];
-                    const CUtensorMap* mb = &maps.m[p.map_b[k.w.it.job]];
-                    const CUtensorMap* mc = &maps.m[p.map_c[k.w.it.job]];
+                    if (!wait(&empty[s], n / S + 1)) { ok = false; break; }
                     const int na = (J.da + 63) / 64, nc = (J.dc + 63) / 64;
                     unsigned char* st = smem + s * Cf::STAGE;
                     tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((outs ? 2 : 1) * na + nc) * 16384));
                     const int t = chunk_time(k.w, k.c, J.reverse);
-                    for (int i = 0; i < na; ++i) {
-                        const int x = k.w.it.h * J.da + 64 * i;
-                        tc::tma_load_3d(st + Cf::A_BYTES + i * 16384, mb, x, t, k.w.b, &full[s]);
-                        if (outs) tc::tma_load_3d(st + i * 16384, ma, x, t, k.w.b, &full[s]);
-                    }
+#pragma unroll 1
+                    for (int i = 0; i < na; ++i)
+                        tc::tma_load_3d(st + Cf::A_BYTES + i * 16384, &maps.m[p.map_b[jn]], h * J.da + 64 * i, t, k.w.b, &full[s]);
+#pragma unroll 1
                     for (int i = 0; i < nc; ++i)
-                        tc::tma_load_3d(st + 2 * Cf::A_BYTES + i * 16384, mc, k.w.it.h * J.dc + 64 * i, t, k.w.b, &full[s]);
+                        tc::tma_load_3d(st + 2 * Cf::A_BYTES + i * 16384, &maps.m[p.map_c[jn]], h * J.dc + 64 * i, t, k.w.b, &full[s]);
+                    if (outs) {
+                        // out of the stage's last chunk leaves before a comes in
+                        if (n >= S) {
+                            if (!store(s, n - S)) { ok = false; break; }
+                            bulk_wait_read();
+                        }
+#pragma unroll
+                        for (int i = 0; i < S; ++i)
+                            if (i == s) {
+                                oj[i] = p.tma_out[jn] && t >= 0 ? jn : -1;
+                                ox[i] = h * J.dc; ot[i] = t; ob[i] = k.w.b;
+                            }
+#pragma unroll 1
+                        for (int i = 0; i < na; ++i)
+                            tc::tma_load_3d(st + i * 16384, &maps.m[p.map_a[jn]], h * J.da + 64 * i, t, k.w.b, &full[s]);
+                    }
                 }
+                if (outs && ok) {
+#pragma unroll 1
+                    for (int i = n > S ? n - S : 0; i < n && ok; ++i) ok = store(i % S, i);
+                }
+                bulk_wait_all();
                 if (*abort_flag) {   // copies in flight land before shared memory is released
                     const uint64_t t0 = globaltimer_ns();
                     for (int i = n > S ? n - S : 0; i < n; ++i)
                         while (!tc::mbar_try_wait(&full[i % S], (uint32_t)((i / S) & 1)) &&
                                globaltimer_ns() - t0 < 100000000ull) {}
+                    // (a stage that got only a part of its loads has them ended by then)
                 }
             }
         } else if (warp == 1 && outs) {
-            // ----------------------------------------- P, a X and P' c
-            int n = 0;          // chunk of a X and P' c
+            // ------------------------------------------------- P and P' c
+            int n = 0;          // chunk of P' c
             int np = 0;         // chunk of P
-            Chunks k, kp;
-            // P of chunk np; it lies over the P' of PB chunks before
+            Chunks k(digits), kp(digits);
+            // P of chunk np; it lies over the P' of PB chunks before, whose product has ended
             auto scores = [&]() {
-                if (!kp.next(p)) return true;
+                if (!kp.next(p, digits)) return true;
                 if (!wait(&full[np % S], np / S)) return false;
-                if (np >= PB && PB == 1 && !wait(bO, np - 1)) return false;
                 tc::tc_fence_after();
-                const int ka = p.g.job[kp.w.it.job].da / 16;
+                const int ka = p.g.job[kp.w.job].da / 16;
                 const uint64_t da = tc::smem_desc_sw128(tc::smem_u32(smem + (np % S) * Cf::STAGE));
                 const uint64_t db = at(da, Cf::A_BYTES);
                 const uint32_t id = tc::instr_desc(1, 128, 128), d = tmem + Cf::cP + (np % PB) * 128;
                 if (tc::elect_one()) {
-#pragma unroll 2
-                    for (int i = 0; i < ka; ++i) {
+#pragma unroll
+                    for (int i = 0; i < DA / 16; ++i) {
+                        if (i >= ka) break;
                         const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
                         tc::mma_bf16(d, at(da, off), at(db, off), id, i != 0);
                     }
@@ -332,54 +442,67 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 return true;
             };
             bool ok = scores();
-            for (; ok && k.next(p); ++n) {
-                const LinJob& J = p.g.job[k.w.it.job];
-                const int s = n % S, ka = J.da / 16;
-                const uint32_t sa = tc::smem_u32(smem + s * Cf::STAGE);
-                const uint64_t da = tc::smem_desc_sw128(sa);
-                const uint64_t dc = tc::smem_desc_sw128_mn(sa + 2 * Cf::A_BYTES, 16384);
-                const uint64_t dx = tc::smem_desc_sw128(tc::smem_u32(sX + (n % XB) * Cf::X_BYTES));
-                const uint32_t idX = tc::instr_desc(1, 128, J.dc), idO = idX | (1u << 16);
-                if (!wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) break;
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
-#pragma unroll 1
-                    for (int h = 0; h < (HALF ? 2 : 1); ++h)
-#pragma unroll 2
-                        for (int i = 0; i < ka; ++i) {
-                            const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
-                            tc::mma_bf16(tmem + Cf::cO, at(da, off), at(dx, off + h * 8192), idX, (h | i) != 0);
-                        }
-                    tc::mma_commit(&bM2[n % XB]);
-                }
-                __syncwarp();
+            for (; ok && k.next(p, digits); ++n) {
+                const int s = n % S;
+                const uint64_t dc = tc::smem_desc_sw128_mn(tc::smem_u32(smem + s * Cf::STAGE + 2 * Cf::A_BYTES), 16384);
+                const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.job].dc) | (1u << 16);
                 // with two score buffers the next chunk's product runs beside this chunk's P'
-                if (PB == 2 && !scores()) break;
-                if (!wait(&bPb[n % PB], n / PB)) break;
+                if (PB == 2 && ((n > 0 && !wait(bO, n - 1)) || !scores())) break;
+                // out's accumulator already holds a X
+                if (!wait(&bM2[n % XB], n / XB) || !wait(&bPb[n % PB], n / PB)) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
-#pragma unroll 2
+#pragma unroll
                     for (int i = 0; i < kC / 16; ++i)
-                        tc::mma_bf16_ts(tmem + Cf::cO, tmem + Cf::cP + (n % PB) * 128 + 8 * i, at(dc, i * 2048), idO, 1);
+                        tc::mma_bf16_ts(tmem + Cf::cO, tmem + Cf::cP + (n % PB) * 128 + 8 * i, at(dc, i * 2048), id, 1);
                     tc::mma_commit(bO);
                     tc::mma_commit(&empty[s]);
                 }
                 __syncwarp();
-                if (PB == 1 && !scores()) break;
+                if (PB == 1 && (!wait(bO, n) || !scores())) break;
             }
             if (*abort_flag) {   // products in flight end before tensor memory is released
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) {}
+            }
+        } else if (warp == 3 && outs) {
+            // ----------------------------------------------------------- a X
+            int n = 0;
+            Chunks k(digits);
+            for (; k.next(p, digits); ++n) {
+                const LinJob& J = p.g.job[k.w.job];
+                const int s = n % S, ka = J.da / 16;
+                const uint64_t da = tc::smem_desc_sw128(tc::smem_u32(smem + s * Cf::STAGE));
+                const uint64_t dx = tc::smem_desc_sw128(tc::smem_u32(sX + (n % XB) * Cf::X_BYTES));
+                const uint32_t id = tc::instr_desc(1, 128, J.dc);
+                if (!wait(&full[s], n / S) || !wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) break;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int h = 0; h < (HALF ? 2 : 1); ++h)
+#pragma unroll
+                        for (int i = 0; i < DA / 16; ++i) {
+                            if (i >= ka) break;
+                            const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
+                            tc::mma_bf16(tmem + Cf::cO, at(da, off), at(dx, off + h * 8192), id, (h | i) != 0);
+                        }
+                    tc::mma_commit(&bM2[n % XB]);
+                }
+                __syncwarp();
+            }
+            if (*abort_flag) {
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) {}
             }
         } else if (warp == 2) {
             // ------------------------------------------------------------ U
             int n = 0;
-            Chunks k;
+            Chunks k(digits);
             bool ok = true;
-            for (; ok && k.next(p); ++n) {
+            for (; ok && k.next(p, digits); ++n) {
                 const int s = n % S;
                 const uint64_t db = tc::smem_desc_sw128_mn(tc::smem_u32(smem + s * Cf::STAGE) + Cf::A_BYTES, 16384);
-                const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.it.job].da) | (1u << 16);
+                const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.job].da) | (1u << 16);
                 if (!wait(&full[s], n / S) || (n > 0 && !wait(bUf, n - 1))) break;
 #pragma unroll 1
                 for (int r = 0; r < kC / kSub; ++r) {
@@ -414,17 +537,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
         int n = 0;
         bool ok = outs;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            Walk w;
-            walk_of(p, item, w);
-            const LinJob& J = p.g.job[w.it.job];
-            const int e = w.it.e, rev = J.reverse;
-            const float ld = out_decay(w.it.ld);
+        Walk w(digits);
+        while (ok && w.next(p, digits)) {
+            const LinJob& J = p.g.job[w.job];
+            const int rev = J.reverse, e = rev ? 0 : 1;
+            const float ld = out_decay(lin_log_decay(p.g.log_decay[w.h]));
             // I*: decays stronger than e^-40 over a chunk take their factors one by one
             const bool by_column = !(ld * (float)kC < -40.0f);
             const int cap = by_column ? 2 * kC : max(1, (int)(40.0f / -ld));
             const int first_pad = !rev && w.c0 == 0 ? w.pad : 0;   // steps missing at the front of the first chunk
-            bf16* o = static_cast<bf16*>(J.o) + (size_t)w.it.h * J.dc;
+            bf16* o = static_cast<bf16*>(J.o) + (size_t)w.h * J.dc;
             tc::named_bar_sync(1, 128);   // the last item's factors are read
             if (by_column) {
                 // g^(-tau_j - e): of the first chunk, then of the others
@@ -445,43 +567,51 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 const uint32_t tp = tl + Cf::cP + (nn % PB) * 128;
                 const float* fc = sf + (c == w.c0 ? 0 : kC);
                 const float* ft = sf + kTabZero - power(c);
+                // blocks of 32 columns that the mask leaves: before the diagonal
+                // one and that, or that and behind; the next one's scores are on
+                // their way while a block is weighed
+                const int k0 = rev ? q : 0, k1 = rev ? 4 : q + 1;
+                float v[2][16];
+                tc::tmem_ld16(tp + k0 * 32, v[0]);
+                tc::tmem_ld16(tp + k0 * 32 + 16, v[1]);
+                uint32_t r[16];
 #pragma unroll 1
-                for (int kb = 0; kb < 4; ++kb) {
-                    uint32_t r[16];
-                    if (rev ? kb < q : kb > q) {
+                for (int kb = k0; kb < k1; ++kb) {
+                    tc::tmem_ld_wait();
+                    if (by_column) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) r[k] = 0;
+                        for (int k = 0; k < 32; k += 4) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fc + kb * 32 + k);
+                            float* x = &v[k >> 4][k & 15];
+                            mul2(x[0], x[1], f.x);
+                            mul2(x[2], x[3], f.y);
+                        }
                     } else {
-                        float v[2][16];
-                        tc::tmem_ld16(tp + kb * 32, v[0]);
-                        tc::tmem_ld16(tp + kb * 32 + 16, v[1]);
-                        tc::tmem_ld_wait();
-                        if (by_column) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fc + kb * 32 + k);
-                                float* x = &v[k >> 4][k & 15];
-                                mul2(x[0], x[1], f.x);
-                                mul2(x[2], x[3], f.y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const int d = rev ? kb * 32 + k - i : i - kb * 32 - k;   // tau_i - tau_j
-                                float& x = v[k >> 4][k & 15];
-                                x = d >= 0 ? x * ft[d] : 0.0f;
-                            }
+                        for (int k = 0; k < 32; ++k) {
+                            const int d = rev ? kb * 32 + k - i : i - kb * 32 - k;   // tau_i - tau_j
+                            float& x = v[k >> 4][k & 15];
+                            x = d >= 0 ? x * ft[d] : 0.0f;
                         }
-                        if (kb == q) {
+                    }
+                    if (kb == q) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (rev ? k < lane : k > lane) v[k >> 4][k & 15] = 0.0f;
-                        }
+                        for (int k = 0; k < 32; ++k)
+                            if (rev ? k < lane : k > lane) v[k >> 4][k & 15] = 0.0f;
+                    }
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) r[k] = pack2(v[k >> 3][(2 * k) & 15], v[k >> 3][(2 * k + 1) & 15]);
+                    for (int k = 0; k < 16; ++k) r[k] = pack2(v[k >> 3][(2 * k) & 15], v[k >> 3][(2 * k + 1) & 15]);
+                    if (kb + 1 < k1) {
+                        tc::tmem_ld16(tp + kb * 32 + 32, v[0]);
+                        tc::tmem_ld16(tp + kb * 32 + 48, v[1]);
                     }
                     tc::tmem_st16(tp + kb * 16, r);
                 }
+                // (these columns held scores that are read by now)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = 0;
+#pragma unroll 1
+                for (int kb = rev ? 0 : q + 1; kb < (rev ? q : 4); ++kb) tc::tmem_st16(tp + kb * 16, r);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -490,8 +620,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             auto write = [&](int c, int nn) {   // out of chunk c
                 const float f = expf(ld * (float)power(c)) * J.oscale;
-                const int t = chunk_time(w, c, rev) + i;
-                uint4* dst = reinterpret_cast<uint4*>(o + w.it.row.padded(t) * J.ldo);
+                const int t0 = chunk_time(w, c, rev), t = t0 + i;
+                const bool tma = p.tma_out[w.job] && t0 >= 0;
+                uint4* dst = reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo);
+                // the row's place among a's: 128-byte rows of 64 columns, swizzled
+                unsigned char* so = smem + (nn % S) * Cf::STAGE + i * 128;
                 if (!wait(bO, nn)) return false;
                 tc::tc_fence_after();
 #pragma unroll 1
@@ -505,46 +638,53 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(bOf);
                     }
-                    if (t < 0) continue;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if (cb + b * 16 >= J.dc) break;
-#pragma unroll
-                        for (int k = 0; k < 16; k += 8) {
-                            const float* x = &v[b][k];
-                            dst[(cb + b * 16 + k) / 8] = make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f),
-                                                                    pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
-                        }
+                    for (int b = 0; b < 4; ++b) {
+                        const float* x = &v[b >> 1][(b & 1) * 8];
+                        const uint4 r = make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f),
+                                                   pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
+                        const int col = cb + b * 8;
+                        if (tma) *reinterpret_cast<uint4*>(so + (col >> 6) * 16384 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) = r;
+                        else if (t >= 0 && col < J.dc) dst[col / 8] = r;
                     }
                 }
+                if (tma) tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bS[nn % S]);
                 return true;
             };
             bool good = true;
-            for (int c = w.c0; c < w.c1 && good; ++c, ++n) {
-                good = weigh(c, n);
-                // with two score buffers out of the chunk before is written while P' c is computed
-                if (PB == 2) good = good && (c == w.c0 || write(c - 1, n - 1));
-                else good = good && write(c, n);
+            if constexpr (PB == 2) {
+                // out of the chunk before is written while P' c is computed
+#pragma unroll 1
+                for (int c = w.c0; w.c0 < w.c1 && c <= w.c1 && good; ++c) {
+                    if (c < w.c1) good = weigh(c, n++);
+                    if (c > w.c0) good = good && write(c - 1, c < w.c1 ? n - 2 : n - 1);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = w.c0; c < w.c1 && good; ++c, ++n) good = weigh(c, n) && write(c, n);
             }
-            if (PB == 2 && good && w.c0 < w.c1) good = write(w.c1 - 1, n - 1);
             // padded steps
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const int per = J.dc / 8;
-            for (int k = i; k < (w.it.pad1 - w.it.pad0) * per; k += 128)
-                *reinterpret_cast<uint4*>(o + w.it.row.padded(w.it.pad0 + k / per) * J.ldo + (k % per) * 8) = zero;
+            const int s1 = min(p.g.T, (w.seg + 1) * p.g.seg_len);
+#pragma unroll 1
+            for (int t = max(w.len, w.seg * p.g.seg_len) + i; t < s1; t += 128)
+#pragma unroll 1
+                for (int k = 0; k < per; ++k) *reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo + k * 8) = zero;
             // the four warps leave together
             if (tc::named_bar_or(1, 128, !good)) ok = false;
         }
     } else if (warp < 12) {
         // ------------------------------------------------ w c
         // A pair of steps at a time in packed bf16, without leaving it: with
-        // w = w0 + w1 + w2 in three bf16 parts,
-        //   p0 = rn(c w0), e = c w0 - p0 (exact: the product has 16 bits),
-        //   p1 = rn(e + c w1), p2 = rn(c w2 + rn(c w1 + rn(e - p1))),
-        // six instructions for two elements, where going through float32
-        // takes seventeen.  ldmatrix turns the tile's rows (steps) into pairs
-        // of steps of one column, as the 16-lane store to tensor memory wants
-        // them.
+        // w = w0 + w1 + w2 in three bf16 parts, a product of two of 8 bits has
+        // 16, so its rounding error is a bf16 number, too:
+        //   p0 = rn(c w0), p1 = c w0 - p0, p2 = rn(c w1), p3 = rn(c w1 - p2 + c w2),
+        // seven instructions for the four parts of two elements.  ldmatrix
+        // turns the tile's rows (steps) into pairs of steps of one column, as
+        // the 16-lane store to tensor memory wants them.
         regs_dec<kRegsWeight>();
         const int q = warp & 3, l = q * 32 + lane;
         const bool second = HALF && q >= 2;         // the rows of the second parts
@@ -556,26 +696,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t u0 = (uint32_t)((unit ^ (row & 7)) << 4), u1 = (uint32_t)(((unit + 2) ^ (row & 7)) << 4);
         int n = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            Walk w;
-            walk_of(p, item, w);
-            const LinJob& J = p.g.job[w.it.job];
-            const int e = w.it.e, rev = J.reverse;
+        Walk w(digits);
+        while (ok && w.next(p, digits)) {
+            const LinJob& J = p.g.job[w.job];
+            const int rev = J.reverse, e = rev ? 0 : 1;
+            const float ld = lin_log_decay(p.g.log_decay[w.h]);
             // w_j of whole chunks and of the reverse's partial one (the
             // forward's partial chunk has zeros where it has no steps)
             tc::named_bar_sync(2, 128);   // the last item's are read
             {
                 const int k = l >> 6, j = (l & 63) * 2;   // variant, pair
+                // a thread of the loop below reads every fourth pair of 16: side by side
+                const int place = (j >> 5) * 16 + ((j >> 1) & 3) * 4 + ((j >> 3) & 3);
                 float f[2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int x = rev ? (k ? kC - w.pad : kC) - (kC - 1 - j - u) : kC - e - j - u;
-                    f[u] = x >= 0 ? expf(w.it.ld * (float)x) * J.bscale : 0.0f;
+                    f[u] = x >= 0 ? expf(ld * (float)x) * J.bscale : 0.0f;
                 }
 #pragma unroll
                 for (int u = 0; u < 3; ++u) {
                     const uint32_t h = pack2(f[0], f[1]);
-                    sw[(k * 3 + u) * (kC / 2) + (l & 63)] = h;
+                    sw[(k * 3 + u) * (kC / 2) + place] = h;
                     f[0] -= lo_half(h);
                     f[1] -= hi_half(h);
                 }
@@ -583,7 +725,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc::named_bar_sync(2, 128);
             bool good = true;
             for (int c = w.c0; c < w.c1 && good; ++c, ++n) {
-                const uint32_t* wj = sw + (rev && c == w.nct - 1 ? 3 * kC / 2 : 0) + (lane & 3);
+                const uint32_t* wj = sw + (rev && c == w.nct - 1 ? 3 * kC / 2 : 0) + (lane & 3) * 4;
                 const int s = n % S;
                 if (!wait(&full[s], n / S)) { good = false; break; }
 #pragma unroll 1
@@ -591,47 +733,55 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const int set = b & 1, turn = n * (kC / kSub / 2) + (b >> 1);
                     const uint32_t src = lm + (uint32_t)(s * Cf::STAGE + b * kSub * 128);
                     // [lane half][8 registers: columns of 8 steps, rows 0-7 and 8-15 of the half]
-                    uint32_t p0[2][8], p1[2][8], p2[2][8];
+                    uint32_t x[2][8];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        ldmatrix_t(src + t * 2048 + u0, &p0[0][4 * t]);
-                        ldmatrix_t(src + t * 2048 + u1, &p0[1][4 * t]);
+                        ldmatrix_t(src + t * 2048 + u0, &x[0][4 * t]);
+                        ldmatrix_t(src + t * 2048 + u1, &x[1][4 * t]);
                     }
+                    uint32_t w0[4], w1[4], w2[4];
+                    lds4(wj + b * 16, w0);
+                    lds4(wj + kC / 2 + b * 16, w1);
+                    lds4(wj + kC + b * 16, w2);
+                    // bf16 pairs: columns of 4 pairs k, rows 0-7 and 8-15 of lane half h
+                    auto part = [&](int which, int h, uint32_t (&r)[8]) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __nv_bfloat162 w0 = as_bf2(wj[b * 16 + 4 * k]), w1 = as_bf2(wj[kC / 2 + b * 16 + 4 * k]),
-                                             w2 = as_bf2(wj[kC + b * 16 + 4 * k]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int u = 2 * k; u < 2 * k + 2; ++u) {
-                                const __nv_bfloat162 x = as_bf2(p0[h][u]);
-                                const __nv_bfloat162 a0 = __hmul2_rn(x, w0);
-                                const __nv_bfloat162 ex = __hfma2(x, w0, __hneg2(a0));
-                                const __nv_bfloat162 a1 = __hfma2(x, w1, ex);
-                                const __nv_bfloat162 a2 = __hfma2(x, w2, __hfma2(x, w1, __hsub2_rn(ex, a1)));
-                                p0[h][u] = as_u32(a0);
-                                p1[h][u] = as_u32(a1);
-                                p2[h][u] = as_u32(a2);
+                        for (int u = 0; u < 8; ++u) {
+                            const __nv_bfloat162 c2 = as_bf2(x[h][u]);
+                            const __nv_bfloat162 v = as_bf2(which < 2 ? w0[u / 2] : w1[u / 2]);
+                            __nv_bfloat162 y = __hmul2_rn(c2, v);
+                            if (which & 1) {
+                                y = __hfma2(c2, v, __hneg2(y));
+                                if (which == 3) y = __hfma2(c2, as_bf2(w2[u / 2]), y);
                             }
-                    }
+                            r[u] = as_u32(y);
+                        }
+                    };
                     if (turn > 0 && !wait(&bWf[set], turn - 1)) { good = false; break; }
                     tc::tc_fence_after();
                     const uint32_t d = tl + set * Cf::PARTS * (kSub / 2);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t dh = d + ((uint32_t)(h * 16) << 16);
+                        uint32_t r[8];
                         if constexpr (HALF) {
                             if (second) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) { p0[h][k] = p1[h][k]; p2[h][k] = 0; }
+                                part(1, h, r);
+                                tmem_st_rows(dh, r);
+                                part(3, h, r);
+                                tmem_st_rows(dh + 16, r);
+                            } else {
+                                part(0, h, r);
+                                tmem_st_rows(dh, r);
+                                part(2, h, r);
+                                tmem_st_rows(dh + 16, r);
                             }
-                            tmem_st_rows(dh, p0[h]);
-                            tmem_st_rows(dh + 16, p2[h]);
                         } else {
-                            tmem_st_rows(dh, p0[h]);
-                            tmem_st_rows(dh + 16, p1[h]);
-                            tmem_st_rows(dh + 32, p2[h]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                part(i, h, r);
+                                tmem_st_rows(dh + i * 16, r);
+                            }
                         }
                     }
                     tc::tmem_st_wait();
@@ -651,18 +801,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + Cf::cU;
         int n = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < p.items && ok; item += gridDim.x) {
-            Walk w;
-            walk_of(p, item, w);
-            const LinJob& J = p.g.job[w.it.job];
-            const float ld = w.it.ld;
+        Walk w(digits);
+        while (ok && w.next(p, digits)) {
+            const LinJob& J = p.g.job[w.job];
+            const float ld = lin_log_decay(p.g.log_decay[w.h]);
+            const float* init;
+            float* fin;
+            bool init_t;
+            state_of(p, w, init, init_t, fin);
             float X[DA];
-            if (w.it.init && !second && r < J.dc) {
+            if (init && !second && r < J.dc) {
 #pragma unroll
                 for (int kb = 0; kb < DA; kb += 16) {
                     if (kb < J.da) {
-                        if (w.it.init_t) {
-                            const float4* x0 = reinterpret_cast<const float4*>(w.it.init + (size_t)r * J.da + kb);
+                        if (init_t) {
+                            const float4* x0 = reinterpret_cast<const float4*>(init + (size_t)r * J.da + kb);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const float4 v = x0[k];
@@ -670,7 +823,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                                 X[kb + 4 * k + 2] = v.z; X[kb + 4 * k + 3] = v.w;
                             }
                         } else {
-                            const float* x0 = w.it.init + (size_t)kb * J.dc + r;
+                            const float* x0 = init + (size_t)kb * J.dc + r;
 #pragma unroll
                             for (int k = 0; k < 16; ++k) X[kb + k] = x0[(size_t)k * J.dc];
                         }
@@ -724,7 +877,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 ++n;
                 if (outs && c + 1 < w.c1) good = put_x();   // the next chunk's
             }
-            if (w.it.fin) {
+            if (fin) {
                 if constexpr (HALF) {
                     // the two sums are added in the place of X's copies, once
                     // the last products that read those have ended
@@ -744,7 +897,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     tc::named_bar_sync(3, 128);
                 }
                 if (!second && r < J.dc) {
-                    float* f = w.it.fin + r;
+                    float* f = fin + r;
 #pragma unroll
                     for (int kb = 0; kb < DA; kb += 16)
                         if (kb < J.da) {
@@ -831,11 +984,16 @@ cudaError_t run_mode(const LinArgs& a, int mode, cudaStream_t s, int* n) {
                 p.map_b[k] = map_of(J.b, J.ldb, J.da);
                 p.map_c[k] = map_of(J.c, J.ldc, J.dc);
                 if (p.map_a[k] < 0 || p.map_b[k] < 0 || p.map_c[k] < 0) return cudaErrorInvalidValue;
+                // out's tile takes a's place: no wider than a, in whole boxes of
+                // 64 columns (a box over the head's end would write the next)
+                p.tma_out[k] = J.dc % 64 == 0 && J.dc <= da && a.T >= kC;
+                if (!make_map(&maps.o[k], a, J.o, J.ldo, (long long)a.H * J.dc)) return cudaErrorInvalidValue;
             }
             if (p.g.njobs == 0) continue;
             // the products of one launch are neighbours in `a`, and so are their states in the buffer
             p.g.buf = a.buf + (size_t)first * a.B * a.H * a.nseg * a.job[0].da * a.job[0].dc;
             p.items = a.B * a.H * p.g.njobs * a.nseg;
+            p.nmaps = nmaps;
             p.mode = mode;
             p.reset = *n == 0;
             p.status = a.status;
