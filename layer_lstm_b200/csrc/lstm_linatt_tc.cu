@@ -26,10 +26,10 @@
 // pipeline that runs across chunks and items, joined by mbarriers only:
 //   warp 0 loads a, b, c and stores out by TMA; warp 1 issues P and P' c, warp 2
 //   U, warp 3 a X;
-//   warps 4-7 (a thread per step) turn P into P' and out into bf16, in the place
-//   of a;
-//   warps 8-11 (a thread per value column) weight c, 32 steps at a time;
-//   warps 12-15 (a thread per value column) carry X.
+//   warps 4-7 (a thread per step) turn P into P';
+//   warps 8-11 (a thread per step) turn out into bf16, in the place of a;
+//   warps 12-15 (a thread per value column) weight c, 32 steps at a time;
+//   warps 16-19 (a thread per value column) carry X.
 // Tensor memory: P (P' over it; two of them for value sizes up to 64) | out | U
 // | w c (two sets of 32 steps).
 //
@@ -50,13 +50,13 @@ namespace lstm {
 namespace {
 
 constexpr int kC = kLinTcChunk;        // steps a chunk
-constexpr int kThreadsTc = 512;
-// Registers a thread of each group of four warps (512 in all at launch): the
-// threads that carry X hold up to 128 sums.
-constexpr int kRegsControl = 96, kRegsOut = 128, kRegsWeight = 104, kRegsCarry = 184;
-static_assert(kRegsControl + kRegsOut + kRegsWeight + kRegsCarry <= 4 * 128, "registers of the block");
+constexpr int kThreadsTc = 640;
+// Registers a thread of each group of four warps (96 at launch): the threads
+// that carry X hold up to 128 sums.
+constexpr int kRegsControl = 72, kRegsScore = 80, kRegsOut = 64, kRegsWeight = 80, kRegsCarry = 184;
+static_assert(kRegsControl + kRegsScore + kRegsOut + kRegsWeight + kRegsCarry <= 5 * 96, "registers of the block");
 constexpr int kSub = 32;               // steps weighted at a time
-constexpr int kTab = 260, kTabZero = 130;   // g^(n), n from -130 to 129
+constexpr int kTab = 322, kTabZero = 192;   // g^(n), n from -192 to 129
 
 struct Params {
     LinArgs g;
@@ -98,8 +98,11 @@ struct Cfg {
 };
 static_assert(Cfg<false, 128>::SMEM <= 232448, "shared memory of one block");
 
-// The decay that the outputs are formed with.
+// The decay that the outputs are formed with, and I*.
 __device__ __forceinline__ float out_decay(float ld) { return ld < -40.0f ? -40.0f : ld; }
+__device__ __forceinline__ int power_cap(float ld) {
+    return ld * (float)kC < -40.0f ? max(1, (int)(40.0f / -ld)) : 2 * kC;
+}
 
 // Where a block is in the list of items, ((job B + b) H + h) nseg + seg, as its
 // digits; the next item is gridDim.x further, added digit by digit (a division
@@ -202,6 +205,23 @@ __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)
                  : "memory");
 }
 
+// Columns of this thread's lane of tensor memory: the wait of one load is some
+// 300 cycles here, however many columns it brings.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+        "}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]),
+          "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]),
+          "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]),
+          "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Tile of shared memory to box {c0, c1, c2} of a tensor, in this thread's bulk group.
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -231,24 +251,16 @@ __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Bounded wait, as tc::mbar_wait in fewer instructions: this kernel's warps run
-// seven programs on each scheduler, and its speed hangs on how much of them the
-// instruction caches hold.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, const Params& p) {
-    uint64_t t0 = 0;
+// Bounded waits in few instructions: this kernel's warps run seven programs on
+// each scheduler, and its speed hangs on how much of them the instruction
+// caches hold.  The loads' warp keeps the time: in its own waits, which end only
+// with the other roles' progress, and then in a wait for the other warps' ends.
+// When it gives up it sets the flag that every other wait looks at.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort) {
     uint32_t i = 0;
 #pragma unroll 1
-    while (!tc::mbar_try_wait(bar, parity)) {
-        if ((++i & 255u) != 0) continue;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if (*abort) return false;
-        if (t - t0 > p.timeout_ns) {
-            atomicCAS(p.status, kStatusOk, kStatusTimeout);
-            *abort = 1;
-            return false;
-        }
-    }
+    while (!tc::mbar_try_wait(bar, parity))
+        if ((++i & 255u) == 0 && *abort) return false;
     return true;
 }
 
@@ -295,7 +307,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint64_t* bM2 = bX + XB;       // [XB] a X computed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bM2 + XB);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* digits = reinterpret_cast<int*>(tmem_slot + 2);   // [8]: the first item's, gridDim.x's
+    volatile int* ended = reinterpret_cast<volatile int*>(tmem_slot + 2);   // warps that are done
+    int* digits = reinterpret_cast<int*>(tmem_slot + 3);   // [8]: the first item's, gridDim.x's
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool outs = p.mode != kLinStates;   // outputs wanted, not only states
@@ -323,6 +336,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc::mbar_init(&bM2[i], 1);
         }
         *abort_flag = 0;
+        *ended = 0;
         digits_of(p, (int)blockIdx.x, digits);
         digits_of(p, (int)gridDim.x, digits + 4);
         tc::fence_mbar_init();
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (uint32_t)(phase & 1), abort_flag, p); };
+    auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (uint32_t)(phase & 1), abort_flag); };
     // descriptor of `d` moved by `bytes`
     auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
 
@@ -346,6 +360,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (warp == 0) {
             // ------------------------------------------------- loads, stores
             if (lane == 0) {
+                auto wait_timed = [&](uint64_t* bar, int phase) {
+                    return tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status, p.timeout_ns);
+                };
                 int n = 0;
                 Chunks k(digits);
                 // where out of the chunk that holds a stage goes: job (-1:
@@ -354,7 +371,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                 for (int s = 0; s < S; ++s) oj[s] = -1;
                 auto store = [&](int s, int nn) {   // out of chunk nn
-                    if (!wait(&bS[s], nn / S)) return false;
+                    if (!wait_timed(&bS[s], nn / S)) return false;
                     int j = -1, x = 0, t = 0, b = 0;
 #pragma unroll
                     for (int i = 0; i < S; ++i)
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     const int jn = k.w.job, h = k.w.h;
                     const LinJob& J = p.g.job[jn];
                     const int s = n % S;
-                    if (!wait(&empty[s], n / S + 1)) { ok = false; break; }
+                    if (!wait_timed(&empty[s], n / S + 1)) { ok = false; break; }
                     const int na = (J.da + 63) / 64, nc = (J.dc + 63) / 64;
                     unsigned char* st = smem + s * Cf::STAGE;
                     tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((outs ? 2 : 1) * na + nc) * 16384));
@@ -404,6 +421,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (outs && ok) {
 #pragma unroll 1
                     for (int i = n > S ? n - S : 0; i < n && ok; ++i) ok = store(i % S, i);
+                }
+                // keeps the time for the warps that are still at work
+                const uint64_t t1 = globaltimer_ns();
+                while (*ended < kThreadsTc / 32 - 1) {
+                    if (globaltimer_ns() - t1 > p.timeout_ns && !*abort_flag) {
+                        atomicCAS(p.status, kStatusOk, kStatusTimeout);
+                        *abort_flag = 1;
+                    }
                 }
                 bulk_wait_all();
                 if (*abort_flag) {   // copies in flight land before shared memory is released
@@ -531,8 +556,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         }
     } else if (warp < 8) {
-        // ------------------------------------------------ P -> P', out
-        regs_dec<kRegsOut>();
+        // ------------------------------------------------ P -> P'
+        regs_dec<kRegsScore>();
         const int q = warp & 3, i = q * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
         int n = 0;
@@ -542,11 +567,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const LinJob& J = p.g.job[w.job];
             const int rev = J.reverse, e = rev ? 0 : 1;
             const float ld = out_decay(lin_log_decay(p.g.log_decay[w.h]));
-            // I*: decays stronger than e^-40 over a chunk take their factors one by one
-            const bool by_column = !(ld * (float)kC < -40.0f);
-            const int cap = by_column ? 2 * kC : max(1, (int)(40.0f / -ld));
+            const int cap = power_cap(ld);
+            // decays stronger than e^-40 over a chunk take their factors one by one
+            const bool by_column = cap > kC;
             const int first_pad = !rev && w.c0 == 0 ? w.pad : 0;   // steps missing at the front of the first chunk
-            bf16* o = static_cast<bf16*>(J.o) + (size_t)w.h * J.dc;
             tc::named_bar_sync(1, 128);   // the last item's factors are read
             if (by_column) {
                 // g^(-tau_j - e): of the first chunk, then of the others
@@ -554,27 +578,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 sf[i] = expf(-ld * (float)(tj - first_pad + e)) * J.bscale;
                 sf[kC + i] = expf(-ld * (float)(tj + e)) * J.bscale;
             } else {
+#pragma unroll 1
                 for (int k = i; k < kTab; k += 128)
                     sf[k] = expf(fminf(ld * (float)(k - kTabZero), 41.0f)) * J.bscale;
             }
             tc::named_bar_sync(1, 128);
-            // the exponent of the step's state term
-            auto power = [&](int c) { return min(max(rev ? kC - 1 - i : i - (c == w.c0 ? first_pad : 0), 0) + e, cap); };
-
-            auto weigh = [&](int c, int nn) {   // P -> P' of chunk c
-                if (!wait(&bP[nn % PB], nn / PB)) return false;
+            bool good = true;
+#pragma unroll 1
+            for (int c = w.c0; c < w.c1; ++c, ++n) {
+                if (!wait(&bP[n % PB], n / PB)) { good = false; break; }
                 tc::tc_fence_after();
-                const uint32_t tp = tl + Cf::cP + (nn % PB) * 128;
+                const uint32_t tp = tl + Cf::cP + (n % PB) * 128;
+                const int pad = c == w.c0 ? first_pad : 0;
                 const float* fc = sf + (c == w.c0 ? 0 : kC);
-                const float* ft = sf + kTabZero - power(c);
-                // blocks of 32 columns that the mask leaves: before the diagonal
-                // one and that, or that and behind; the next one's scores are on
-                // their way while a block is weighed
+                const float* ft = sf + kTabZero - min(max(rev ? kC - 1 - i : i - pad, 0) + e, cap);
+                // blocks of 32 columns that the mask leaves: up to the diagonal
+                // one, or from it on; the next one's scores are on their way
+                // while a block is weighed
                 const int k0 = rev ? q : 0, k1 = rev ? 4 : q + 1;
-                float v[2][16];
-                tc::tmem_ld16(tp + k0 * 32, v[0]);
-                tc::tmem_ld16(tp + k0 * 32 + 16, v[1]);
+                float v[32];
                 uint32_t r[16];
+                tmem_ld(tp + k0 * 32, v);
 #pragma unroll 1
                 for (int kb = k0; kb < k1; ++kb) {
                     tc::tmem_ld_wait();
@@ -582,29 +606,24 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4) {
                             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(fc + kb * 32 + k);
-                            float* x = &v[k >> 4][k & 15];
-                            mul2(x[0], x[1], f.x);
-                            mul2(x[2], x[3], f.y);
+                            mul2(v[k], v[k + 1], f.x);
+                            mul2(v[k + 2], v[k + 3], f.y);
                         }
                     } else {
+                        // by tau_i - tau_j (what the mask takes lies at negative ones)
+                        const float* fi = ft + (rev ? kb * 32 - i : i - kb * 32);
+                        const int step = rev ? 1 : -1;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int d = rev ? kb * 32 + k - i : i - kb * 32 - k;   // tau_i - tau_j
-                            float& x = v[k >> 4][k & 15];
-                            x = d >= 0 ? x * ft[d] : 0.0f;
-                        }
+                        for (int k = 0; k < 32; ++k) v[k] *= fi[k * step];
                     }
                     if (kb == q) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (rev ? k < lane : k > lane) v[k >> 4][k & 15] = 0.0f;
+                            if (rev ? k < lane : k > lane) v[k] = 0.0f;
                     }
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) r[k] = pack2(v[k >> 3][(2 * k) & 15], v[k >> 3][(2 * k + 1) & 15]);
-                    if (kb + 1 < k1) {
-                        tc::tmem_ld16(tp + kb * 32 + 32, v[0]);
-                        tc::tmem_ld16(tp + kb * 32 + 48, v[1]);
-                    }
+                    for (int k = 0; k < 16; ++k) r[k] = pack2(v[2 * k], v[2 * k + 1]);
+                    if (kb + 1 < k1) tmem_ld(tp + kb * 32 + 32, v);
                     tc::tmem_st16(tp + kb * 16, r);
                 }
                 // (these columns held scores that are read by now)
@@ -615,68 +634,82 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bPb[nn % PB]);
-                return true;
-            };
-            auto write = [&](int c, int nn) {   // out of chunk c
-                const float f = expf(ld * (float)power(c)) * J.oscale;
-                const int t0 = chunk_time(w, c, rev), t = t0 + i;
-                const bool tma = p.tma_out[w.job] && t0 >= 0;
-                uint4* dst = reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo);
-                // the row's place among a's: 128-byte rows of 64 columns, swizzled
-                unsigned char* so = smem + (nn % S) * Cf::STAGE + i * 128;
-                if (!wait(bO, nn)) return false;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int cb = 0; cb < J.dc; cb += 32) {
-                    float v[2][16];
-                    tc::tmem_ld16(tl + Cf::cO + cb, v[0]);
-                    tc::tmem_ld16(tl + Cf::cO + cb + 16, v[1]);
-                    tc::tmem_ld_wait();
-                    if (cb + 32 >= J.dc) {   // all of out is in registers
-                        tc::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(bOf);
-                    }
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const float* x = &v[b >> 1][(b & 1) * 8];
-                        const uint4 r = make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f),
-                                                   pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
-                        const int col = cb + b * 8;
-                        if (tma) *reinterpret_cast<uint4*>(so + (col >> 6) * 16384 + ((((col & 63) >> 3) ^ (i & 7)) << 4)) = r;
-                        else if (t >= 0 && col < J.dc) dst[col / 8] = r;
-                    }
-                }
-                if (tma) tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bS[nn % S]);
-                return true;
-            };
-            bool good = true;
-            if constexpr (PB == 2) {
-                // out of the chunk before is written while P' c is computed
-#pragma unroll 1
-                for (int c = w.c0; w.c0 < w.c1 && c <= w.c1 && good; ++c) {
-                    if (c < w.c1) good = weigh(c, n++);
-                    if (c > w.c0) good = good && write(c - 1, c < w.c1 ? n - 2 : n - 1);
-                }
-            } else {
-#pragma unroll 1
-                for (int c = w.c0; c < w.c1 && good; ++c, ++n) good = weigh(c, n) && write(c, n);
+                if (lane == 0) tc::mbar_arrive(&bPb[n % PB]);
             }
-            // padded steps
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const int per = J.dc / 8;
-            const int s1 = min(p.g.T, (w.seg + 1) * p.g.seg_len);
-#pragma unroll 1
-            for (int t = max(w.len, w.seg * p.g.seg_len) + i; t < s1; t += 128)
-#pragma unroll 1
-                for (int k = 0; k < per; ++k) *reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo + k * 8) = zero;
             // the four warps leave together
             if (tc::named_bar_or(1, 128, !good)) ok = false;
         }
     } else if (warp < 12) {
+        // ------------------------------------------------ out
+        regs_dec<kRegsOut>();
+        const int q = warp & 3, i = q * 32 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + Cf::cO;
+        int n = 0;
+        bool ok = outs;
+        Walk w(digits);
+        while (ok && w.next(p, digits)) {
+            const LinJob& J = p.g.job[w.job];
+            const int rev = J.reverse, e = rev ? 0 : 1;
+            const float ld = out_decay(lin_log_decay(p.g.log_decay[w.h]));
+            const int cap = power_cap(ld);
+            bf16* o = static_cast<bf16*>(J.o) + (size_t)w.h * J.dc;
+            bool good = true;
+#pragma unroll 1
+            for (int c = w.c0; c < w.c1; ++c, ++n) {
+                // g to the exponent of the step's state term
+                const int tau = rev ? kC - 1 - i : i - (c == 0 ? w.pad : 0);
+                const float f = expf(ld * (float)min(max(tau, 0) + e, cap)) * J.oscale;
+                const int t0 = chunk_time(w, c, rev), t = t0 + i;
+                const bool tma = p.tma_out[w.job] && t0 >= 0;
+                uint4* dst = reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo);
+                // the row's place among a's: 128-byte rows of 64 columns, swizzled
+                unsigned char* so = smem + (n % S) * Cf::STAGE + i * 128;
+                if (!wait(bO, n)) { good = false; break; }
+                tc::tc_fence_after();
+                float v[32];
+                tmem_ld(tl, v);
+#pragma unroll 1
+                for (int cb = 0; cb < J.dc; cb += 32) {
+                    tc::tmem_ld_wait();
+                    uint4 r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float* x = v + k * 8;
+                        r[k] = make_uint4(pack2(x[0] * f, x[1] * f), pack2(x[2] * f, x[3] * f),
+                                          pack2(x[4] * f, x[5] * f), pack2(x[6] * f, x[7] * f));
+                    }
+                    if (cb + 32 < J.dc) {
+                        tmem_ld(tl + cb + 32, v);
+                    } else {   // all of out is in registers
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(bOf);
+                    }
+                    if (tma) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(so + (cb >> 6) * 16384 + ((((cb & 32) / 8 + k) ^ (i & 7)) << 4)) = r[k];
+                    } else if (t >= 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (cb + k * 8 < J.dc) dst[cb / 8 + k] = r[k];
+                    }
+                }
+                if (tma) tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bS[n % S]);
+            }
+            // padded steps
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const int s1 = min(p.g.T, (w.seg + 1) * p.g.seg_len);
+#pragma unroll 1
+            for (int t = max(w.len, w.seg * p.g.seg_len) + i; t < s1; t += 128)
+#pragma unroll 1
+                for (int k = 0; k < J.dc / 8; ++k)
+                    *reinterpret_cast<uint4*>(o + time_row(p, w.b, t) * J.ldo + k * 8) = zero;
+            if (tc::named_bar_or(4, 128, !good)) ok = false;
+        }
+    } else if (warp < 16) {
         // ------------------------------------------------ w c
         // A pair of steps at a time in packed bf16, without leaving it: with
         // w = w0 + w1 + w2 in three bf16 parts, a product of two of 8 bits has
@@ -860,16 +893,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
                 for (int kb = 0; kb < DA; kb += 32) {
                     if (kb >= J.da) break;
-                    float v[16], u[16];
-                    tc::tmem_ld16(tl + kb, v);
-                    if (kb + 16 < J.da) tc::tmem_ld16(tl + kb + 16, u);
+                    float v[32];
+                    tmem_ld(tl + kb, v);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) X[kb + k] = fmaf(gm, X[kb + k], v[k]);
-                    if (kb + 16 < J.da) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) X[kb + 16 + k] = fmaf(gm, X[kb + 16 + k], u[k]);
-                    }
+                    for (int k = 0; k < 32; ++k) X[kb + k] = fmaf(gm, X[kb + k], v[k]);
                 }
                 tc::tc_fence_before();
                 __syncwarp();
@@ -909,6 +937,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (tc::named_bar_or(3, 128, !good)) ok = false;
         }
     }
+    if (warp != 0 && lane == 0) atomicAdd(const_cast<int*>(ended), 1);
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
