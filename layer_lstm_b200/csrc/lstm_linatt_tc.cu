@@ -31,7 +31,7 @@
 //   warps 12-15 (a thread per value column) weight c, 32 steps at a time;
 //   warps 16-19 (a thread per value column) carry X.
 // Tensor memory: P (P' over it; two of them for value sizes up to 64) | out | U
-// | w c (two sets of 32 steps).
+// | w c (sets of 32 steps).
 //
 // Bound: HBM (four rows of 2 d bytes a step).  A chunk's products take an
 // eighth of its load time on the tensor cores; what has to fit beside the
@@ -89,12 +89,13 @@ struct Cfg {
     static constexpr int XB = HALF || DA == 64 ? 2 : 1;    // copies of X
     static constexpr int PB = HALF ? 2 : 1;                // scores in tensor memory
     static constexpr int PARTS = HALF ? 2 : 4;             // operands that hold w c
+    static constexpr int SETS = 2;                             // sets of 32 steps of them
     static constexpr int TAB_BYTES = (2 * 3 * kC / 2 + kTab) * 4;
-    static constexpr int BARS = 3 * S + 8 + 2 * XB + 2 * PB;
+    static constexpr int BARS = 3 * S + 4 + 2 * SETS + 2 * XB + 2 * PB;
     static constexpr size_t SMEM = (size_t)S * STAGE + XB * X_BYTES + TAB_BYTES + BARS * 8 + 48;
     // tensor-memory columns; a set of w c takes 16 of them for each operand
     static constexpr int cP = 0, cO = PB * 128, cU = cO + DCP, cW = cU + DA;
-    static_assert(cW + 2 * PARTS * kSub / 2 <= 512, "tensor memory");
+    static_assert(cW + SETS * PARTS * kSub / 2 <= 512, "tensor memory");
 };
 static_assert(Cfg<false, 128>::SMEM <= 232448, "shared memory of one block");
 
@@ -285,7 +286,7 @@ template <bool HALF, int DA>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     lin_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Cf = Cfg<HALF, DA>;
-    constexpr int S = Cf::S, XB = Cf::XB, PB = Cf::PB;
+    constexpr int S = Cf::S, XB = Cf::XB, PB = Cf::PB, SETS = Cf::SETS;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char* sX = smem + S * Cf::STAGE;
     // w of each pair of steps in three bf16 parts [2][3][kC / 2]: whole chunks,
@@ -299,9 +300,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint64_t* bPb = bP + PB;       // [PB] P' written
     uint64_t* bO = bPb + PB;       // out computed
     uint64_t* bOf = bO + 1;        // out read
-    uint64_t* bW = bOf + 1;        // [2] w c written
-    uint64_t* bWf = bW + 2;        // [2] w c read by the products
-    uint64_t* bU = bWf + 2;        // U computed
+    uint64_t* bW = bOf + 1;        // [SETS] w c written
+    uint64_t* bWf = bW + SETS;     // [SETS] w c read by the products
+    uint64_t* bU = bWf + SETS;     // U computed
     uint64_t* bUf = bU + 1;        // U read
     uint64_t* bX = bUf + 1;        // [XB] X written
     uint64_t* bM2 = bX + XB;       // [XB] a X computed
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         tc::mbar_init(bO, 1);
         tc::mbar_init(bOf, 4);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < SETS; ++i) {
             tc::mbar_init(&bW[i], 4);
             tc::mbar_init(&bWf[i], 1);
         }
@@ -359,85 +360,89 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         regs_dec<kRegsControl>();
         if (warp == 0) {
             // ------------------------------------------------- loads, stores
-            if (lane == 0) {
-                auto wait_timed = [&](uint64_t* bar, int phase) {
-                    return tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status, p.timeout_ns);
-                };
-                int n = 0;
-                Chunks k(digits);
-                // where out of the chunk that holds a stage goes: job (-1:
-                // nowhere by TMA), columns, time, batch row
-                int oj[S], ox[S], ot[S], ob[S];
+            // (the whole warp waits, one lane issues: a wait by one lane of a
+            // diverged warp takes 600 cycles, by the warp 100)
+            auto wait_timed = [&](uint64_t* bar, int phase) {
+                return tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status, p.timeout_ns);
+            };
+            int n = 0;
+            Chunks k(digits);
+            // where out of the chunk that holds a stage goes: job (-1:
+            // nowhere by TMA), columns, time, batch row
+            int oj[S], ox[S], ot[S], ob[S];
 #pragma unroll
-                for (int s = 0; s < S; ++s) oj[s] = -1;
-                auto store = [&](int s, int nn) {   // out of chunk nn
-                    if (!wait_timed(&bS[s], nn / S)) return false;
-                    int j = -1, x = 0, t = 0, b = 0;
+            for (int s = 0; s < S; ++s) oj[s] = -1;
+            auto store = [&](int s, int nn) {   // out of chunk nn
+                if (!wait_timed(&bS[s], nn / S)) return false;
+                int j = -1, x = 0, t = 0, b = 0;
+#pragma unroll
+                for (int i = 0; i < S; ++i)
+                    if (i == s) { j = oj[i]; x = ox[i]; t = ot[i]; b = ob[i]; }
+                if (j >= 0 && lane == 0) {
+                    tma_store_3d(&maps.o[j], smem + s * Cf::STAGE, x, t, b);
+                    if (p.g.job[j].dc > 64) tma_store_3d(&maps.o[j], smem + s * Cf::STAGE + 16384, x + 64, t, b);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = true;
+            for (; k.next(p, digits); ++n) {
+                const int jn = k.w.job, h = k.w.h;
+                const LinJob& J = p.g.job[jn];
+                const int s = n % S;
+                if (!wait_timed(&empty[s], n / S + 1)) { ok = false; break; }
+                unsigned char* st = smem + s * Cf::STAGE;
+                const int t = chunk_time(k.w, k.c, J.reverse);
+                const bool a2 = DA == 128 && J.da > 64, c2 = !HALF && J.dc > 64;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&full[s], (uint32_t)((outs ? 2 : 1) * (a2 ? 2 : 1) + (c2 ? 2 : 1)) * 16384u);
+                    const CUtensorMap* mb = &maps.m[p.map_b[jn]];
+                    const CUtensorMap* mc = &maps.m[p.map_c[jn]];
+                    tc::tma_load_3d(st + Cf::A_BYTES, mb, h * J.da, t, k.w.b, &full[s]);
+                    if (a2) tc::tma_load_3d(st + Cf::A_BYTES + 16384, mb, h * J.da + 64, t, k.w.b, &full[s]);
+                    tc::tma_load_3d(st + 2 * Cf::A_BYTES, mc, h * J.dc, t, k.w.b, &full[s]);
+                    if (c2) tc::tma_load_3d(st + 2 * Cf::A_BYTES + 16384, mc, h * J.dc + 64, t, k.w.b, &full[s]);
+                }
+                __syncwarp();
+                if (outs) {
+                    // out of the stage's last chunk leaves before a comes in
+                    if (n >= S && !store(s, n - S)) { ok = false; break; }
 #pragma unroll
                     for (int i = 0; i < S; ++i)
-                        if (i == s) { j = oj[i]; x = ox[i]; t = ot[i]; b = ob[i]; }
-                    if (j >= 0) {
-                        const int nc = p.g.job[j].dc / 64;
-#pragma unroll 1
-                        for (int i = 0; i < nc; ++i)
-                            tma_store_3d(&maps.o[j], smem + s * Cf::STAGE + i * 16384, x + 64 * i, t, b);
-                        bulk_commit();
-                    }
-                    return true;
-                };
-                bool ok = true;
-                for (; k.next(p, digits); ++n) {
-                    const int jn = k.w.job, h = k.w.h;
-                    const LinJob& J = p.g.job[jn];
-                    const int s = n % S;
-                    if (!wait_timed(&empty[s], n / S + 1)) { ok = false; break; }
-                    const int na = (J.da + 63) / 64, nc = (J.dc + 63) / 64;
-                    unsigned char* st = smem + s * Cf::STAGE;
-                    tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(((outs ? 2 : 1) * na + nc) * 16384));
-                    const int t = chunk_time(k.w, k.c, J.reverse);
-#pragma unroll 1
-                    for (int i = 0; i < na; ++i)
-                        tc::tma_load_3d(st + Cf::A_BYTES + i * 16384, &maps.m[p.map_b[jn]], h * J.da + 64 * i, t, k.w.b, &full[s]);
-#pragma unroll 1
-                    for (int i = 0; i < nc; ++i)
-                        tc::tma_load_3d(st + 2 * Cf::A_BYTES + i * 16384, &maps.m[p.map_c[jn]], h * J.dc + 64 * i, t, k.w.b, &full[s]);
-                    if (outs) {
-                        // out of the stage's last chunk leaves before a comes in
-                        if (n >= S) {
-                            if (!store(s, n - S)) { ok = false; break; }
-                            bulk_wait_read();
+                        if (i == s) {
+                            oj[i] = p.tma_out[jn] && t >= 0 ? jn : -1;
+                            ox[i] = h * J.dc; ot[i] = t; ob[i] = k.w.b;
                         }
-#pragma unroll
-                        for (int i = 0; i < S; ++i)
-                            if (i == s) {
-                                oj[i] = p.tma_out[jn] && t >= 0 ? jn : -1;
-                                ox[i] = h * J.dc; ot[i] = t; ob[i] = k.w.b;
-                            }
-#pragma unroll 1
-                        for (int i = 0; i < na; ++i)
-                            tc::tma_load_3d(st + i * 16384, &maps.m[p.map_a[jn]], h * J.da + 64 * i, t, k.w.b, &full[s]);
+                    if (lane == 0) {
+                        const CUtensorMap* ma = &maps.m[p.map_a[jn]];
+                        tc::tma_load_3d(st, ma, h * J.da, t, k.w.b, &full[s]);
+                        if (a2) tc::tma_load_3d(st + 16384, ma, h * J.da + 64, t, k.w.b, &full[s]);
                     }
+                    __syncwarp();
                 }
-                if (outs && ok) {
+            }
+            if (outs && ok) {
 #pragma unroll 1
-                    for (int i = n > S ? n - S : 0; i < n && ok; ++i) ok = store(i % S, i);
+                for (int i = n > S ? n - S : 0; i < n && ok; ++i) ok = store(i % S, i);
+            }
+            // keeps the time for the warps that are still at work
+            const uint64_t t1 = globaltimer_ns();
+            while (*ended < kThreadsTc / 32 - 1) {
+                if (globaltimer_ns() - t1 > p.timeout_ns && !*abort_flag) {
+                    atomicCAS(p.status, kStatusOk, kStatusTimeout);
+                    *abort_flag = 1;
                 }
-                // keeps the time for the warps that are still at work
-                const uint64_t t1 = globaltimer_ns();
-                while (*ended < kThreadsTc / 32 - 1) {
-                    if (globaltimer_ns() - t1 > p.timeout_ns && !*abort_flag) {
-                        atomicCAS(p.status, kStatusOk, kStatusTimeout);
-                        *abort_flag = 1;
-                    }
-                }
-                bulk_wait_all();
-                if (*abort_flag) {   // copies in flight land before shared memory is released
-                    const uint64_t t0 = globaltimer_ns();
-                    for (int i = n > S ? n - S : 0; i < n; ++i)
-                        while (!tc::mbar_try_wait(&full[i % S], (uint32_t)((i / S) & 1)) &&
-                               globaltimer_ns() - t0 < 100000000ull) {}
-                    // (a stage that got only a part of its loads has them ended by then)
-                }
+            }
+            __syncwarp();
+            if (lane == 0) bulk_wait_all();
+            if (*abort_flag) {   // copies in flight land before shared memory is released
+                const uint64_t t0 = globaltimer_ns();
+                for (int i = n > S ? n - S : 0; i <= n; ++i)
+                    while (!tc::mbar_try_wait(&full[i % S], (uint32_t)((i / S) & 1)) &&
+                           globaltimer_ns() - t0 < 100000000ull) {}
+                // (a stage that got only a part of its loads has them ended by then)
             }
         } else if (warp == 1 && outs) {
             // ------------------------------------------------- P and P' c
@@ -454,9 +459,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 const uint64_t db = at(da, Cf::A_BYTES);
                 const uint32_t id = tc::instr_desc(1, 128, 128), d = tmem + Cf::cP + (np % PB) * 128;
                 if (tc::elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < DA / 16; ++i) {
-                        if (i >= ka) break;
+#pragma unroll 2
+                    for (int i = 0; i < ka; ++i) {
                         const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
                         tc::mma_bf16(d, at(da, off), at(db, off), id, i != 0);
                     }
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!wait(&bM2[n % XB], n / XB) || !wait(&bPb[n % PB], n / PB)) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
-#pragma unroll
+#pragma unroll 2
                     for (int i = 0; i < kC / 16; ++i)
                         tc::mma_bf16_ts(tmem + Cf::cO, tmem + Cf::cP + (n % PB) * 128 + 8 * i, at(dc, i * 2048), id, 1);
                     tc::mma_commit(bO);
@@ -503,11 +507,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!wait(&full[s], n / S) || !wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < (HALF ? 2 : 1); ++h)
-#pragma unroll
-                        for (int i = 0; i < DA / 16; ++i) {
-                            if (i >= ka) break;
+#pragma unroll 2
+                        for (int i = 0; i < ka; ++i) {
                             const uint32_t off = (uint32_t)((i >> 2) * 16384 + (i & 3) * 32);
                             tc::mma_bf16(tmem + Cf::cO, at(da, off), at(dx, off + h * 8192), id, (h | i) != 0);
                         }
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!wait(&full[s], n / S) || (n > 0 && !wait(bUf, n - 1))) break;
 #pragma unroll 1
                 for (int r = 0; r < kC / kSub; ++r) {
-                    const int set = r & 1, turn = n * (kC / kSub / 2) + (r >> 1);
+                    const int set = r % SETS, turn = n * (kC / kSub / SETS) + r / SETS;
                     if (!wait(&bW[set], turn)) { ok = false; break; }
                     tc::tc_fence_after();
                     if (tc::elect_one()) {
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 if (!wait(&full[s], n / S)) { good = false; break; }
 #pragma unroll 1
                 for (int b = 0; b < kC / kSub; ++b) {
-                    const int set = b & 1, turn = n * (kC / kSub / 2) + (b >> 1);
+                    const int set = b % SETS, turn = n * (kC / kSub / SETS) + b / SETS;
                     const uint32_t src = lm + (uint32_t)(s * Cf::STAGE + b * kSub * 128);
                     // [lane half][8 registers: columns of 8 steps, rows 0-7 and 8-15 of the half]
                     uint32_t x[2][8];
