@@ -47,42 +47,57 @@ __device__ __forceinline__ uint32_t pcg(uint32_t x) {
     return (w >> 22) ^ w;
 }
 
+// Small whole numbers to float32 and back by the exponent of 2^23 (the
+// conversion instructions run at an eighth of the rate of an addition, and
+// eight of them per element would take as long as the rest).
+__device__ __forceinline__ float small_float(uint32_t n) { return __uint_as_float(0x4B000000u | n) - 8388608.0f; }
+__device__ __forceinline__ uint32_t small_bits(float x) { return __float_as_uint(x + 8388608.0f); }   // low bytes: x
+
 // Code c of a first moment stands for sign (c / 127)^2 a, of a second for
 // (c / 255)^4 a, with a the largest magnitude of the element's block of 256.
 // The codes are dense where the values are small next to the block's largest:
 // the smallest nonzero first moment is 6e-5 a, second moment 2e-10 a.
-__device__ __forceinline__ float decode_m(int c, float a) {
-    const float q = __fmul_rn((float)c, 1.0f / 127.0f);
+__device__ __forceinline__ float decode_m(float c, float a) {
+    const float q = __fmul_rn(c, 1.0f / 127.0f);
     return __fmul_rn(__fmul_rn(fabsf(q), q), a);
 }
-__device__ __forceinline__ float decode_v(int c, float a) {
-    const float q = __fmul_rn((float)c, 1.0f / 255.0f);
+__device__ __forceinline__ float decode_v(float c, float a) {
+    const float q = __fmul_rn(c, 1.0f / 255.0f);
     const float q2 = __fmul_rn(q, q);
     return __fmul_rn(__fmul_rn(q2, q2), a);
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Rounds up with the probability that keeps the mean of the value the code
 // stands for: rounding to the nearest code would hold a second moment still
 // for as long as a step changes it by less than half a code, which at
-// b2 = 0.999 is nearly always.  z = |x| / a; u random in [0, 1).
-__device__ __forceinline__ int encode_m(float z, float u) {
+// b2 = 0.999 is nearly always.  z = |x| / a; u random in [0, 1).  The root may
+// be off by its last bits: where that moves floor() by one, x lies within them
+// of a code, and either start leads to that code (below it, the gap to it
+// exceeds u times the gap; at it, nothing remains to round up).
+__device__ __forceinline__ float encode_m(float z, float u) {
     const float X = __fmul_rn(z, 16129.0f);
-    float c = floorf(__fsqrt_rn(X));
+    float c = floorf(sqrt_approx(X));
     const float lo = __fmul_rn(c, c), c1 = __fadd_rn(c, 1.0f), hi = __fmul_rn(c1, c1);
     if (__fmul_rn(u, __fsub_rn(hi, lo)) < __fsub_rn(X, lo)) c = c1;
-    return (int)fminf(c, 127.0f);
+    return fminf(c, 127.0f);
 }
 // A second moment that is not zero keeps a code of at least 1: a zero under
 // the root would let the next step divide by eps alone.
-__device__ __forceinline__ int encode_v(float z, float u) {
+__device__ __forceinline__ float encode_v(float z, float u) {
     const float X = __fmul_rn(z, 4228250625.0f);
-    float c = floorf(__fsqrt_rn(__fsqrt_rn(X)));
+    float c = floorf(sqrt_approx(sqrt_approx(X)));
     const float c1 = __fadd_rn(c, 1.0f);
     const float lo2 = __fmul_rn(c, c), hi2 = __fmul_rn(c1, c1);
     const float lo = __fmul_rn(lo2, lo2), hi = __fmul_rn(hi2, hi2);
     if (__fmul_rn(u, __fsub_rn(hi, lo)) < __fsub_rn(X, lo)) c = c1;
     if (X > 0.0f) c = fmaxf(c, 1.0f);
-    return (int)fminf(c, 255.0f);
+    return fminf(c, 255.0f);
 }
 
 struct Coef {
@@ -90,20 +105,24 @@ struct Coef {
     uint32_t k1;                  // random key of (seed, step)
 };
 
-__device__ __forceinline__ Coef make_coef(const Params& P) {
+// Warp 0 and warp 1 each take a power in float64 (a microsecond).
+__device__ __forceinline__ void make_coef(const Params& P, Coef& c) {
+    if ((threadIdx.x & 31) != 0 || threadIdx.x >= 64) return;
     const long long t = *P.step + 1;
-    double lr = P.lr;
-    Coef c;
-    c.gs = 1.0f;
-    if (P.scalars) {
-        lr *= (double)P.scalars[0];
-        c.gs = P.scalars[1];
+    if (threadIdx.x == 0) {
+        double lr = P.lr;
+        float gs = 1.0f;
+        if (P.scalars) {
+            lr *= (double)P.scalars[0];
+            gs = P.scalars[1];
+        }
+        c.size = (float)(lr / (1.0 - pow(P.beta1, (double)t)));
+        c.keep = (float)(1.0 - lr * P.wd);
+        c.gs = gs;
+    } else {
+        c.root = (float)(1.0 / sqrt(1.0 - pow(P.beta2, (double)t)));
+        c.k1 = pcg((uint32_t)t ^ pcg((uint32_t)P.seed ^ pcg((uint32_t)(P.seed >> 32))));
     }
-    c.size = (float)(lr / (1.0 - pow(P.beta1, (double)t)));
-    c.root = (float)(1.0 / sqrt(1.0 - pow(P.beta2, (double)t)));
-    c.keep = (float)(1.0 - lr * P.wd);
-    c.k1 = pcg((uint32_t)t ^ pcg((uint32_t)P.seed ^ pcg((uint32_t)(P.seed >> 32))));
-    return c;
 }
 
 __device__ __forceinline__ void update(float& p, float g, float& m, float& v, const Params& P, const Coef& c) {
@@ -124,15 +143,22 @@ __device__ __forceinline__ void get4(const T* x, long long e, long long n, bool 
         for (int i = 0; i < 4; ++i) v[i] = e + i < n ? to_f(x[e + i]) : 0.0f;
     }
 }
-template <typename C>
-__device__ __forceinline__ void get_codes(const C* x, long long e, long long n, bool vec, int (&v)[4]) {
-    if (vec && e + 4 <= n) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(x + e);
+// Four codes as the bytes of a word.
+__device__ __forceinline__ uint32_t get_codes(const void* p, long long e, long long n, bool vec) {
+    const uint8_t* x = static_cast<const uint8_t*>(p);
+    if (vec && e + 4 <= n) return *reinterpret_cast<const uint32_t*>(x + e);
+    uint32_t w = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (int)(C)(w >> (8 * i));
-    } else {
+    for (int i = 0; i < 4; ++i) w |= e + i < n ? (uint32_t)x[e + i] << (8 * i) : 0u;
+    return w;
+}
+// Values of four first-moment codes (signed bytes) and second-moment codes.
+__device__ __forceinline__ void decode4(uint32_t cm, uint32_t cv, float am, float av, float (&m)[4], float (&v)[4]) {
+    cm ^= 0x80808080u;   // signed byte + 128
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = e + i < n ? (int)x[e + i] : 0;
+    for (int i = 0; i < 4; ++i) {
+        m[i] = decode_m(small_float((cm >> (8 * i)) & 255u) - 128.0f, am);
+        v[i] = decode_v(small_float((cv >> (8 * i)) & 255u), av);
     }
 }
 __device__ __forceinline__ void put4(float* x, long long e, long long n, bool vec, const float (&v)[4]) {
@@ -156,14 +182,14 @@ __device__ __forceinline__ void put4(bf16* x, long long e, long long n, bool vec
             if (e + i < n) x[e + i] = __float2bfloat16_rn(v[i]);
     }
 }
-__device__ __forceinline__ void put_codes(uint8_t* x, long long e, long long n, bool vec, const int (&v)[4]) {
+__device__ __forceinline__ void put_codes(void* p, long long e, long long n, bool vec, uint32_t w) {
+    uint8_t* x = static_cast<uint8_t*>(p);
     if (vec && e + 4 <= n) {
-        *reinterpret_cast<uint32_t*>(x + e) = (uint32_t)(v[0] & 255) | (uint32_t)(v[1] & 255) << 8 |
-                                              (uint32_t)(v[2] & 255) << 16 | (uint32_t)(v[3] & 255) << 24;
+        *reinterpret_cast<uint32_t*>(x + e) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (e + i < n) x[e + i] = (uint8_t)v[i];
+            if (e + i < n) x[e + i] = (uint8_t)(w >> (8 * i));
     }
 }
 
@@ -178,125 +204,153 @@ __device__ __forceinline__ int find_tensor(const Table& tab, long long t) {
     return lo;
 }
 
-// Largest value of the warp; NaN if any lane holds one.
+// Largest magnitude; NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
 __device__ __forceinline__ float warp_max_nan(float a) {
-    bool bad = !(a == a);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    return __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fc00000) : a;
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(a));
+    return r;
 }
 
+// What a warp holds of one block of 256 elements: 2 x 4 of each lane.
+template <int BITS>
+struct Piece {
+    int ti;              // tensor; -1: none
+    long long base;      // its first element
+    float p[2][4], g[2][4];
+    float m[2][4], v[2][4];   // BITS 32
+    uint32_t cm[2], cv[2];    // BITS 8
+    float am, av;
+};
+
 template <typename G, int BITS>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Params P) {
+__device__ __forceinline__ void load_piece(const Table& tab, long long tile, Piece<BITS>& x) {
+    x.ti = -1;
+    if (tile >= tab.tile_end[tab.count - 1]) return;
+    const int ti = find_tensor(tab, tile);
+    const AdamwTensor& t = tab.t[ti];
+    const bool vec = tab.vec[ti] != 0;
+    const long long n = t.n;
+    x.base = (tile - (ti ? tab.tile_end[ti - 1] : 0)) * kTile + (threadIdx.x >> 5) * kAdamwBlock;
+    if (x.base >= n) return;   // (the whole warp)
+    x.ti = ti;
+    const long long e0 = x.base + (threadIdx.x & 31) * 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const long long e = e0 + j * 128;
+        get4(t.p, e, n, vec, x.p[j]);
+        get4(static_cast<const G*>(t.g), e, n, vec, x.g[j]);
+        if constexpr (BITS == 8) {
+            x.cm[j] = get_codes(t.m, e, n, vec);
+            x.cv[j] = get_codes(t.v, e, n, vec);
+        } else {
+            get4(static_cast<const float*>(t.m), e, n, vec, x.m[j]);
+            get4(static_cast<const float*>(t.v), e, n, vec, x.v[j]);
+        }
+    }
+    if constexpr (BITS == 8) {
+        x.am = t.ms[x.base / kAdamwBlock];
+        x.av = t.vs[x.base / kAdamwBlock];
+    }
+}
+
+// A warp per block of 256 elements, the next block's loads issued before the
+// current one is computed (the first one's before the coefficients).
+template <typename G, int BITS>
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2) adamw_kernel(const __grid_constant__ Params P) {
     __shared__ Coef coef;
-    if (threadIdx.x == 0) coef = make_coef(P);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Table& tab = P.tab;
+    Piece<BITS> x;
+    load_piece<G, BITS>(tab, blockIdx.x, x);
+    make_coef(P, coef);
     __syncthreads();
     const Coef c = coef;
-    const Table& tab = P.tab;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const long long tiles = tab.tile_end[tab.count - 1];
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int ti = find_tensor(tab, tile);
-        const AdamwTensor& t = tab.t[ti];
-        const bool vec = tab.vec[ti] != 0;
-        const long long base = (tile - (ti ? tab.tile_end[ti - 1] : 0)) * kTile + warp * kAdamwBlock;
-        const long long n = t.n;
-        if (base >= n) continue;   // the whole warp: base is the warp's
-        const G* g = static_cast<const G*>(t.g);
-        float p[2][4], gg[2][4], m[2][4], v[2][4];
-        const long long e0 = base + lane * 4;
-        if constexpr (BITS == 8) {
-            const long long blk = base / kAdamwBlock;
-            const float ams = t.ms[blk], avs = t.vs[blk];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                int cm[4], cv[4];
-                get_codes(static_cast<const int8_t*>(t.m), e0 + j * 128, n, vec, cm);
-                get_codes(static_cast<const uint8_t*>(t.v), e0 + j * 128, n, vec, cv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { m[j][i] = decode_m(cm[i], ams); v[j][i] = decode_v(cv[i], avs); }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                get4(static_cast<const float*>(t.m), e0 + j * 128, n, vec, m[j]);
-                get4(static_cast<const float*>(t.v), e0 + j * 128, n, vec, v[j]);
-            }
-        }
+        const Piece<BITS> w = x;
+        load_piece<G, BITS>(tab, tile + gridDim.x, x);
+        if (w.ti < 0) continue;
+        const AdamwTensor& t = tab.t[w.ti];
+        const bool vec = tab.vec[w.ti] != 0;
+        const long long n = t.n, e0 = w.base + lane * 4;
+        const bool whole = w.base + kAdamwBlock <= n;
+        float p[2][4], m[2][4], v[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            get4(t.p, e0 + j * 128, n, vec, p[j]);
-            get4(g, e0 + j * 128, n, vec, gg[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
+            if constexpr (BITS == 8) decode4(w.cm[j], w.cv[j], w.am, w.av, m[j], v[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                update(p[j][i], gg[j][i], m[j][i], v[j][i], P, c);
-                // past the end nothing counts towards the block's scale
-                if (BITS == 8 && e0 + j * 128 + i >= n) m[j][i] = v[j][i] = 0.0f;
+                p[j][i] = w.p[j][i];
+                if constexpr (BITS == 32) { m[j][i] = w.m[j][i]; v[j][i] = w.v[j][i]; }
+                update(p[j][i], w.g[j][i], m[j][i], v[j][i], P, c);
             }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
             put4(t.p, e0 + j * 128, n, vec, p[j]);
             if (t.copy) put4(static_cast<bf16*>(t.copy), e0 + j * 128, n, vec, p[j]);
-        }
-        if constexpr (BITS == 32) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            if constexpr (BITS == 32) {
                 put4(static_cast<float*>(t.m), e0 + j * 128, n, vec, m[j]);
                 put4(static_cast<float*>(t.v), e0 + j * 128, n, vec, v[j]);
             }
-        } else {
+        }
+        if constexpr (BITS == 8) {
             // A block with a NaN or an infinity decodes to NaN as a whole
             // (scale NaN); one whose largest magnitude is below float32's
             // normal range, or zero, to zero.
-            const float inf = __int_as_float(0x7f800000);
+            const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
             float am = 0.0f, av = 0.0f;
-            bool badm = false, badv = false;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    am = fmaxf(am, fabsf(m[j][i]));
-                    av = fmaxf(av, fabsf(v[j][i]));
-                    badm = badm || !(m[j][i] == m[j][i]);
-                    badv = badv || !(v[j][i] == v[j][i]);
+                    // past the end nothing counts towards the block's scale
+                    if (!whole && e0 + j * 128 + i >= n) m[j][i] = v[j][i] = 0.0f;
+                    am = max_nan(am, m[j][i]);
+                    av = max_nan(av, v[j][i]);
                 }
-            am = warp_max_nan(badm ? __int_as_float(0x7fc00000) : am);
-            av = warp_max_nan(badv ? __int_as_float(0x7fc00000) : av);
+            am = warp_max_nan(am);
+            av = warp_max_nan(av);
             const bool finem = am < inf, finev = av < inf;
             const bool somem = finem && am >= 1.17549435e-38f, somev = finev && av >= 1.17549435e-38f;
-            const float im = somem ? __fdiv_rn(1.0f, am) : 0.0f, iv = somev ? __fdiv_rn(1.0f, av) : 0.0f;
-            const uint32_t key = pcg(c.k1 ^ (uint32_t)(tab.first + ti));
+            const float im = somem ? __frcp_rn(am) : 0.0f, iv = somev ? __frcp_rn(av) : 0.0f;
+            const uint32_t key = pcg(c.k1 ^ (uint32_t)(tab.first + w.ti)) ^ (uint32_t)((unsigned long long)w.base >> 32) * 0x9E3779B9u;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                int cm[4], cv[4];
+                uint32_t cm = 0, cv = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const unsigned long long e = (unsigned long long)(e0 + j * 128 + i);
-                    const uint32_t r = pcg((uint32_t)e ^ key ^ (uint32_t)(e >> 32) * 0x9E3779B9u);
-                    const float um = (float)(r & 0xffffu) * 1.52587890625e-05f;
-                    const float uv = (float)(r >> 16) * 1.52587890625e-05f;
+                    const uint32_t r = pcg((uint32_t)(e0 + j * 128 + i) ^ key);
+                    const float um = small_float(r & 0xffffu) * 1.52587890625e-05f;
+                    const float uv = small_float(r >> 16) * 1.52587890625e-05f;
+                    // where the block has no scale the products are 0 or NaN, and 0 is stored
                     const float zm = somem ? fminf(__fmul_rn(fabsf(m[j][i]), im), 1.0f) : 0.0f;
                     const float zv = somev ? fminf(__fmul_rn(fabsf(v[j][i]), iv), 1.0f) : 0.0f;
-                    const int k = encode_m(zm, um);
-                    cm[i] = m[j][i] < 0.0f ? -k : k;
-                    cv[i] = encode_v(zv, uv);
+                    const float k = encode_m(zm, um);
+                    // two's complement of a negative code by its bits around 2^23
+                    cm |= (small_bits(m[j][i] < 0.0f ? 256.0f - k : k) & 255u) << (8 * i);
+                    cv |= (small_bits(encode_v(zv, uv)) & 255u) << (8 * i);
                 }
-                put_codes(static_cast<uint8_t*>(t.m), e0 + j * 128, n, vec, cm);
-                put_codes(static_cast<uint8_t*>(t.v), e0 + j * 128, n, vec, cv);
+                put_codes(t.m, e0 + j * 128, n, vec, cm);
+                put_codes(t.v, e0 + j * 128, n, vec, cv);
             }
             if (lane == 0) {
-                const long long blk = base / kAdamwBlock;
-                t.ms[blk] = somem ? am : (finem ? 0.0f : __int_as_float(0x7fc00000));
-                t.vs[blk] = somev ? av : (finev ? 0.0f : __int_as_float(0x7fc00000));
+                const long long blk = w.base / kAdamwBlock;
+                t.ms[blk] = somem ? am : (finem ? 0.0f : nan);
+                t.vs[blk] = somev ? av : (finev ? 0.0f : nan);
             }
         }
     }
 }
 
-__global__ void adamw_advance_kernel(long long* step) { *step += 1; }
+// Runs behind the last launch of a step, as its programmatic dependent.
+__global__ void adamw_advance_kernel(long long* step) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    *step += 1;
+}
 
 struct ReadParams {
     Table tab;
@@ -320,12 +374,8 @@ __global__ void __launch_bounds__(kThreads) adamw_read_kernel(const __grid_const
         const long long e0 = base + lane * 4;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            int cm[4], cv[4];
             float m[4], v[4];
-            get_codes(static_cast<const int8_t*>(t.m), e0 + j * 128, t.n, vec, cm);
-            get_codes(static_cast<const uint8_t*>(t.v), e0 + j * 128, t.n, vec, cv);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { m[i] = decode_m(cm[i], am); v[i] = decode_v(cv[i], av); }
+            decode4(get_codes(t.m, e0 + j * 128, t.n, vec), get_codes(t.v, e0 + j * 128, t.n, vec), am, av, m, v);
             put4(P.m_out[ti], e0 + j * 128, t.n, vec, m);
             put4(P.v_out[ti], e0 + j * 128, t.n, vec, v);
         }
@@ -363,7 +413,8 @@ cudaError_t launch_adamw(const void* args, cudaStream_t s, int* nlaunch) {
     P.eps = (float)a.eps;
     P.seed = a.seed; P.step = a.step; P.scalars = a.scalars;
     if (tiles > 0) {
-        const int grid = (int)(tiles < (long long)a.num_sms * 4 ? tiles : (long long)a.num_sms * 4);
+        const int per_sm = a.bits == 8 ? 3 : 2;   // blocks an SM, as the launch bounds say
+        const int grid = (int)(tiles < (long long)a.num_sms * per_sm ? tiles : (long long)a.num_sms * per_sm);
         const bool gf = a.gdt == DType::F32;
         if (a.bits == 32) {
             if (gf) adamw_kernel<float, 32><<<grid, kThreads, 0, s>>>(P);
@@ -377,8 +428,16 @@ cudaError_t launch_adamw(const void* args, cudaStream_t s, int* nlaunch) {
         ++*nlaunch;
     }
     if (a.advance) {
-        adamw_advance_kernel<<<1, 1, 0, s>>>(a.step);
-        const cudaError_t e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(1);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, adamw_advance_kernel, a.step);
         if (e != cudaSuccess) return e;
         ++*nlaunch;
     }
