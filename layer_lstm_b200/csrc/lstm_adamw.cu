@@ -10,10 +10,10 @@
 // bounds it.  The tensors' table travels in the kernel's parameters, so a
 // call needs no copy to the device and can be captured into a graph.
 //
-// Every operation below is rounded on its own (no contraction to FMA): the
-// 8-bit codes depend on the last bit of what is encoded, and with one order
-// of roundings they are a function of the inputs that does not move with the
-// compiler's choices.
+// The moments and their codes are rounded operation by operation (no
+// contraction to FMA): the codes depend on the last bit of what is encoded,
+// and with one order of roundings they are a function of the inputs that does
+// not move with the compiler's choices.
 #include "lstm_device.cuh"
 #include "lstm_ops.h"
 
@@ -47,11 +47,12 @@ __device__ __forceinline__ uint32_t pcg(uint32_t x) {
     return (w >> 22) ^ w;
 }
 
-// Small whole numbers to float32 and back by the exponent of 2^23 (the
-// conversion instructions run at an eighth of the rate of an addition, and
-// eight of them per element would take as long as the rest).
-__device__ __forceinline__ float small_float(uint32_t n) { return __uint_as_float(0x4B000000u | n) - 8388608.0f; }
-__device__ __forceinline__ uint32_t small_bits(float x) { return __float_as_uint(x + 8388608.0f); }   // low bytes: x
+// Byte k of w as a float32, by the exponent of 2^23: the conversion
+// instructions run at an eighth of the rate of an addition.  `off` is what the
+// byte is above the number it stands for.
+__device__ __forceinline__ float byte_float(uint32_t w, int k, float off) {
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + k)) - (8388608.0f + off);
+}
 
 // Code c of a first moment stands for sign (c / 127)^2 a, of a second for
 // (c / 255)^4 a, with a the largest magnitude of the element's block of 256.
@@ -67,37 +68,44 @@ __device__ __forceinline__ float decode_v(float c, float a) {
     return __fmul_rn(__fmul_rn(q2, q2), a);
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {
+__device__ __forceinline__ float sqrt_ftz(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
 // Rounds up with the probability that keeps the mean of the value the code
 // stands for: rounding to the nearest code would hold a second moment still
 // for as long as a step changes it by less than half a code, which at
-// b2 = 0.999 is nearly always.  z = |x| / a; u random in [0, 1).  The root may
-// be off by its last bits: where that moves floor() by one, x lies within them
-// of a code, and either start leads to that code (below it, the gap to it
-// exceeds u times the gap; at it, nothing remains to round up).
-__device__ __forceinline__ float encode_m(float z, float u) {
+// b2 = 0.999 is nearly always.  z = |x| / a <= 1; u a random whole number below
+// 2^16.  With X = z 127^2 and c the whole part of its root, up if
+// u / 2^16 ((c + 1)^2 - c^2) < X - c^2.  The root may be off by its last bits:
+// where that moves c by one, X lies within them of a code, and either start
+// leads to that code (below it, the gap to it exceeds u / 2^16 times the gap;
+// at it, nothing remains to round up).  So the largest code is not passed.
+__device__ __forceinline__ uint32_t encode_m(float z, float u) {
     const float X = __fmul_rn(z, 16129.0f);
-    float c = floorf(sqrt_approx(X));
-    const float lo = __fmul_rn(c, c), c1 = __fadd_rn(c, 1.0f), hi = __fmul_rn(c1, c1);
-    if (__fmul_rn(u, __fsub_rn(hi, lo)) < __fsub_rn(X, lo)) c = c1;
-    return fminf(c, 127.0f);
+    const float f = __fadd_rd(sqrt_ftz(X), 8388608.0f);   // the whole part, in the low bits
+    const float c = f - 8388608.0f;
+    const float gap = fmaf(c, 0x1p-15f, 0x1p-16f);        // 2^-16 (2 c + 1), exact
+    return (__float_as_uint(f) & 255u) + (__fmul_rn(u, gap) < __fsub_rn(X, __fmul_rn(c, c)) ? 1u : 0u);
 }
-// A second moment that is not zero keeps a code of at least 1: a zero under
-// the root would let the next step divide by eps alone.
-__device__ __forceinline__ float encode_v(float z, float u) {
+// X = z 255^4 and the fourth powers.  A second moment that is not zero keeps a
+// code of at least 1: a zero under the root would let the next step divide by
+// eps alone.
+__device__ __forceinline__ uint32_t encode_v(float z, float u) {
     const float X = __fmul_rn(z, 4228250625.0f);
-    float c = floorf(sqrt_approx(sqrt_approx(X)));
-    const float c1 = __fadd_rn(c, 1.0f);
-    const float lo2 = __fmul_rn(c, c), hi2 = __fmul_rn(c1, c1);
-    const float lo = __fmul_rn(lo2, lo2), hi = __fmul_rn(hi2, hi2);
-    if (__fmul_rn(u, __fsub_rn(hi, lo)) < __fsub_rn(X, lo)) c = c1;
-    if (X > 0.0f) c = fmaxf(c, 1.0f);
-    return fminf(c, 255.0f);
+    const float f = __fadd_rd(sqrt_ftz(sqrt_ftz(X)), 8388608.0f);
+    const float c = f - 8388608.0f;
+    const float lo2 = __fmul_rn(c, c), hi2 = __fadd_rn(lo2, fmaf(c, 2.0f, 1.0f));
+    const float lo = __fmul_rn(lo2, lo2), gap = __fsub_rn(__fmul_rn(hi2, hi2), lo);
+    const uint32_t k = (__float_as_uint(f) & 255u) + (__fmul_rn(u * 0x1p-16f, gap) < __fsub_rn(X, lo) ? 1u : 0u);
+    return max(k, X > 0.0f ? 1u : 0u);
 }
 
 struct Coef {
@@ -125,18 +133,22 @@ __device__ __forceinline__ void make_coef(const Params& P, Coef& c) {
     }
 }
 
+// The root and the quotient of the update are the approximate ones (2^-22 of
+// it together, under float32's step of p itself for any update below p / 4);
+// the moments are rounded operation by operation.
 __device__ __forceinline__ void update(float& p, float g, float& m, float& v, const Params& P, const Coef& c) {
     g = __fmul_rn(g, c.gs);
     m = __fadd_rn(__fmul_rn(m, P.b1), __fmul_rn(g, P.c1));
     v = __fadd_rn(__fmul_rn(v, P.b2), __fmul_rn(__fmul_rn(g, g), P.c2));
-    const float den = __fadd_rn(__fmul_rn(__fsqrt_rn(v), c.root), P.eps);
-    p = __fsub_rn(__fmul_rn(p, c.keep), __fmul_rn(c.size, __fdiv_rn(m, den)));
+    const float den = fmaf(sqrt_approx(v), c.root, P.eps);
+    p = fmaf(p, c.keep, -c.size * __fdividef(m, den));
 }
 
-// Four elements from e (e < n), as float; zeros past the end.
-template <typename T>
-__device__ __forceinline__ void get4(const T* x, long long e, long long n, bool vec, float (&v)[4]) {
-    if (vec && e + 4 <= n) {
+// Four elements from e as float, zeros past n.  FAST: all four exist and lie
+// on a 16-byte (bf16: 8-byte, codes: 4-byte) boundary.
+template <bool FAST, typename T>
+__device__ __forceinline__ void get4(const T* x, long long e, long long n, float (&v)[4]) {
+    if constexpr (FAST) {
         load4(x + e, v);
     } else {
 #pragma unroll
@@ -144,9 +156,10 @@ __device__ __forceinline__ void get4(const T* x, long long e, long long n, bool 
     }
 }
 // Four codes as the bytes of a word.
-__device__ __forceinline__ uint32_t get_codes(const void* p, long long e, long long n, bool vec) {
+template <bool FAST>
+__device__ __forceinline__ uint32_t get_codes(const void* p, long long e, long long n) {
     const uint8_t* x = static_cast<const uint8_t*>(p);
-    if (vec && e + 4 <= n) return *reinterpret_cast<const uint32_t*>(x + e);
+    if constexpr (FAST) return *reinterpret_cast<const uint32_t*>(x + e);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w |= e + i < n ? (uint32_t)x[e + i] << (8 * i) : 0u;
@@ -157,12 +170,13 @@ __device__ __forceinline__ void decode4(uint32_t cm, uint32_t cv, float am, floa
     cm ^= 0x80808080u;   // signed byte + 128
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        m[i] = decode_m(small_float((cm >> (8 * i)) & 255u) - 128.0f, am);
-        v[i] = decode_v(small_float((cv >> (8 * i)) & 255u), av);
+        m[i] = decode_m(byte_float(cm, i, 128.0f), am);
+        v[i] = decode_v(byte_float(cv, i, 0.0f), av);
     }
 }
-__device__ __forceinline__ void put4(float* x, long long e, long long n, bool vec, const float (&v)[4]) {
-    if (vec && e + 4 <= n) {
+template <bool FAST>
+__device__ __forceinline__ void put4(float* x, long long e, long long n, const float (&v)[4]) {
+    if constexpr (FAST) {
         *reinterpret_cast<float4*>(x + e) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
@@ -171,8 +185,9 @@ __device__ __forceinline__ void put4(float* x, long long e, long long n, bool ve
     }
 }
 // The copy is rounded to nearest even; p itself stays float32.
-__device__ __forceinline__ void put4(bf16* x, long long e, long long n, bool vec, const float (&v)[4]) {
-    if (vec && e + 4 <= n) {
+template <bool FAST>
+__device__ __forceinline__ void put4(bf16* x, long long e, long long n, const float (&v)[4]) {
+    if constexpr (FAST) {
         const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
         *reinterpret_cast<uint2*>(x + e) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
                                                       *reinterpret_cast<const uint32_t*>(&b));
@@ -182,9 +197,10 @@ __device__ __forceinline__ void put4(bf16* x, long long e, long long n, bool vec
             if (e + i < n) x[e + i] = __float2bfloat16_rn(v[i]);
     }
 }
-__device__ __forceinline__ void put_codes(void* p, long long e, long long n, bool vec, uint32_t w) {
+template <bool FAST>
+__device__ __forceinline__ void put_codes(void* p, long long e, long long n, uint32_t w) {
     uint8_t* x = static_cast<uint8_t*>(p);
-    if (vec && e + 4 <= n) {
+    if constexpr (FAST) {
         *reinterpret_cast<uint32_t*>(x + e) = w;
     } else {
 #pragma unroll
@@ -220,6 +236,7 @@ __device__ __forceinline__ float warp_max_nan(float a) {
 template <int BITS>
 struct Piece {
     int ti;              // tensor; -1: none
+    bool fast;           // all 256 exist, on the boundaries of 4-element accesses
     long long base;      // its first element
     float p[2][4], g[2][4];
     float m[2][4], v[2][4];   // BITS 32
@@ -227,34 +244,113 @@ struct Piece {
     float am, av;
 };
 
-template <typename G, int BITS>
-__device__ __forceinline__ void load_piece(const Table& tab, long long tile, Piece<BITS>& x) {
-    x.ti = -1;
-    if (tile >= tab.tile_end[tab.count - 1]) return;
-    const int ti = find_tensor(tab, tile);
-    const AdamwTensor& t = tab.t[ti];
-    const bool vec = tab.vec[ti] != 0;
-    const long long n = t.n;
-    x.base = (tile - (ti ? tab.tile_end[ti - 1] : 0)) * kTile + (threadIdx.x >> 5) * kAdamwBlock;
-    if (x.base >= n) return;   // (the whole warp)
-    x.ti = ti;
+// Finds the warp's block of tile `tile`; false when there is none.
+__device__ __forceinline__ bool find_piece(const Table& tab, long long tile, int& ti, long long& base, bool& fast) {
+    ti = -1;
+    if (tile >= tab.tile_end[tab.count - 1]) return false;
+    const int i = find_tensor(tab, tile);
+    base = (tile - (i ? tab.tile_end[i - 1] : 0)) * kTile + (threadIdx.x >> 5) * kAdamwBlock;
+    if (base >= tab.t[i].n) return false;   // (the whole warp)
+    ti = i;
+    fast = tab.vec[i] != 0 && base + kAdamwBlock <= tab.t[i].n;
+    return true;
+}
+
+template <bool FAST, typename G, int BITS>
+__device__ __forceinline__ void load_elements(const AdamwTensor& t, Piece<BITS>& x) {
     const long long e0 = x.base + (threadIdx.x & 31) * 4;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const long long e = e0 + j * 128;
-        get4(t.p, e, n, vec, x.p[j]);
-        get4(static_cast<const G*>(t.g), e, n, vec, x.g[j]);
+        get4<FAST>(t.p, e, t.n, x.p[j]);
+        get4<FAST>(static_cast<const G*>(t.g), e, t.n, x.g[j]);
         if constexpr (BITS == 8) {
-            x.cm[j] = get_codes(t.m, e, n, vec);
-            x.cv[j] = get_codes(t.v, e, n, vec);
+            x.cm[j] = get_codes<FAST>(t.m, e, t.n);
+            x.cv[j] = get_codes<FAST>(t.v, e, t.n);
         } else {
-            get4(static_cast<const float*>(t.m), e, n, vec, x.m[j]);
-            get4(static_cast<const float*>(t.v), e, n, vec, x.v[j]);
+            get4<FAST>(static_cast<const float*>(t.m), e, t.n, x.m[j]);
+            get4<FAST>(static_cast<const float*>(t.v), e, t.n, x.v[j]);
         }
     }
+}
+
+template <typename G, int BITS>
+__device__ __forceinline__ void load_piece(const Table& tab, long long tile, Piece<BITS>& x) {
+    if (!find_piece(tab, tile, x.ti, x.base, x.fast)) return;
+    const AdamwTensor& t = tab.t[x.ti];
+    if (x.fast) load_elements<true, G>(t, x);
+    else load_elements<false, G>(t, x);
     if constexpr (BITS == 8) {
         x.am = t.ms[x.base / kAdamwBlock];
         x.av = t.vs[x.base / kAdamwBlock];
+    }
+}
+
+template <bool FAST, int BITS>
+__device__ __forceinline__ void step_piece(const Params& P, const Coef& c, const Piece<BITS>& w) {
+    const AdamwTensor& t = P.tab.t[w.ti];
+    const int lane = threadIdx.x & 31;
+    const long long n = t.n, e0 = w.base + lane * 4;
+    float p[2][4], m[2][4], v[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (BITS == 8) decode4(w.cm[j], w.cv[j], w.am, w.av, m[j], v[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[j][i] = w.p[j][i];
+            if constexpr (BITS == 32) { m[j][i] = w.m[j][i]; v[j][i] = w.v[j][i]; }
+            update(p[j][i], w.g[j][i], m[j][i], v[j][i], P, c);
+        }
+        put4<FAST>(t.p, e0 + j * 128, n, p[j]);
+        if (t.copy) put4<FAST>(static_cast<bf16*>(t.copy), e0 + j * 128, n, p[j]);
+        if constexpr (BITS == 32) {
+            put4<FAST>(static_cast<float*>(t.m), e0 + j * 128, n, m[j]);
+            put4<FAST>(static_cast<float*>(t.v), e0 + j * 128, n, v[j]);
+        }
+    }
+    if constexpr (BITS == 8) {
+        // A block with a NaN or an infinity decodes to NaN as a whole (scale
+        // NaN, whatever the codes); one whose largest magnitude is below
+        // float32's normal range, or zero, to zero.
+        const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
+        float am = 0.0f, av = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // past the end nothing counts towards the block's scale
+                if (!FAST && e0 + j * 128 + i >= n) m[j][i] = v[j][i] = 0.0f;
+                am = max_nan(am, m[j][i]);
+                av = max_nan(av, v[j][i]);
+            }
+        am = warp_max_nan(am);
+        av = warp_max_nan(av);
+        const bool finem = am < inf, finev = av < inf;
+        const bool somem = finem && am >= 1.17549435e-38f, somev = finev && av >= 1.17549435e-38f;
+        const float im = somem ? __frcp_rn(am) : 0.0f, iv = somev ? __frcp_rn(av) : 0.0f;
+        const uint32_t key = pcg(c.k1 ^ (uint32_t)(P.tab.first + w.ti)) ^
+                             (uint32_t)((unsigned long long)w.base >> 32) * 0x9E3779B9u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t cm = 0, cv = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = pcg((uint32_t)(e0 + j * 128 + i) ^ key);
+                const float um = __uint_as_float((r & 0xffffu) | 0x4B000000u) - 8388608.0f;
+                const float uv = __uint_as_float(__byte_perm(r, 0x4B000000u, 0x7432u)) - 8388608.0f;
+                const uint32_t k = encode_m(fminf(__fmul_rn(fabsf(m[j][i]), im), 1.0f), um);
+                const uint32_t sign = (uint32_t)(__float_as_int(m[j][i]) >> 31);   // all ones below zero
+                cm |= (((k ^ sign) - sign) & 255u) << (8 * i);
+                cv |= encode_v(fminf(__fmul_rn(v[j][i], iv), 1.0f), uv) << (8 * i);
+            }
+            put_codes<FAST>(t.m, e0 + j * 128, n, cm);
+            put_codes<FAST>(t.v, e0 + j * 128, n, cv);
+        }
+        if (lane == 0) {
+            const long long blk = w.base / kAdamwBlock;
+            t.ms[blk] = somem ? am : (finem ? 0.0f : nan);
+            t.vs[blk] = somev ? av : (finev ? 0.0f : nan);
+        }
     }
 }
 
@@ -264,85 +360,18 @@ template <typename G, int BITS>
 __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2) adamw_kernel(const __grid_constant__ Params P) {
     __shared__ Coef coef;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Table& tab = P.tab;
     Piece<BITS> x;
-    load_piece<G, BITS>(tab, blockIdx.x, x);
+    load_piece<G, BITS>(P.tab, blockIdx.x, x);
     make_coef(P, coef);
     __syncthreads();
     const Coef c = coef;
-    const int lane = threadIdx.x & 31;
-    const long long tiles = tab.tile_end[tab.count - 1];
+    const long long tiles = P.tab.tile_end[P.tab.count - 1];
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const Piece<BITS> w = x;
-        load_piece<G, BITS>(tab, tile + gridDim.x, x);
+        load_piece<G, BITS>(P.tab, tile + gridDim.x, x);
         if (w.ti < 0) continue;
-        const AdamwTensor& t = tab.t[w.ti];
-        const bool vec = tab.vec[w.ti] != 0;
-        const long long n = t.n, e0 = w.base + lane * 4;
-        const bool whole = w.base + kAdamwBlock <= n;
-        float p[2][4], m[2][4], v[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (BITS == 8) decode4(w.cm[j], w.cv[j], w.am, w.av, m[j], v[j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[j][i] = w.p[j][i];
-                if constexpr (BITS == 32) { m[j][i] = w.m[j][i]; v[j][i] = w.v[j][i]; }
-                update(p[j][i], w.g[j][i], m[j][i], v[j][i], P, c);
-            }
-            put4(t.p, e0 + j * 128, n, vec, p[j]);
-            if (t.copy) put4(static_cast<bf16*>(t.copy), e0 + j * 128, n, vec, p[j]);
-            if constexpr (BITS == 32) {
-                put4(static_cast<float*>(t.m), e0 + j * 128, n, vec, m[j]);
-                put4(static_cast<float*>(t.v), e0 + j * 128, n, vec, v[j]);
-            }
-        }
-        if constexpr (BITS == 8) {
-            // A block with a NaN or an infinity decodes to NaN as a whole
-            // (scale NaN); one whose largest magnitude is below float32's
-            // normal range, or zero, to zero.
-            const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
-            float am = 0.0f, av = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // past the end nothing counts towards the block's scale
-                    if (!whole && e0 + j * 128 + i >= n) m[j][i] = v[j][i] = 0.0f;
-                    am = max_nan(am, m[j][i]);
-                    av = max_nan(av, v[j][i]);
-                }
-            am = warp_max_nan(am);
-            av = warp_max_nan(av);
-            const bool finem = am < inf, finev = av < inf;
-            const bool somem = finem && am >= 1.17549435e-38f, somev = finev && av >= 1.17549435e-38f;
-            const float im = somem ? __frcp_rn(am) : 0.0f, iv = somev ? __frcp_rn(av) : 0.0f;
-            const uint32_t key = pcg(c.k1 ^ (uint32_t)(tab.first + w.ti)) ^ (uint32_t)((unsigned long long)w.base >> 32) * 0x9E3779B9u;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t cm = 0, cv = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t r = pcg((uint32_t)(e0 + j * 128 + i) ^ key);
-                    const float um = small_float(r & 0xffffu) * 1.52587890625e-05f;
-                    const float uv = small_float(r >> 16) * 1.52587890625e-05f;
-                    // where the block has no scale the products are 0 or NaN, and 0 is stored
-                    const float zm = somem ? fminf(__fmul_rn(fabsf(m[j][i]), im), 1.0f) : 0.0f;
-                    const float zv = somev ? fminf(__fmul_rn(fabsf(v[j][i]), iv), 1.0f) : 0.0f;
-                    const float k = encode_m(zm, um);
-                    // two's complement of a negative code by its bits around 2^23
-                    cm |= (small_bits(m[j][i] < 0.0f ? 256.0f - k : k) & 255u) << (8 * i);
-                    cv |= (small_bits(encode_v(zv, uv)) & 255u) << (8 * i);
-                }
-                put_codes(t.m, e0 + j * 128, n, vec, cm);
-                put_codes(t.v, e0 + j * 128, n, vec, cv);
-            }
-            if (lane == 0) {
-                const long long blk = w.base / kAdamwBlock;
-                t.ms[blk] = somem ? am : (finem ? 0.0f : nan);
-                t.vs[blk] = somev ? av : (finev ? 0.0f : nan);
-            }
-        }
+        if (w.fast) step_piece<true>(P, c, w);
+        else step_piece<false>(P, c, w);
     }
 }
 
@@ -358,26 +387,47 @@ struct ReadParams {
     float* v_out[kAdamwTensors];
 };
 
-// The 8-bit moments as float32 values.
-__global__ void __launch_bounds__(kThreads) adamw_read_kernel(const __grid_constant__ ReadParams P) {
+// The 8-bit moments as float32 values; two blocks of 256 a warp at a time.
+__global__ void __launch_bounds__(kThreads, 6) adamw_read_kernel(const __grid_constant__ ReadParams P) {
     const Table& tab = P.tab;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     const long long tiles = tab.tile_end[tab.count - 1];
-    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int ti = find_tensor(tab, tile);
-        const AdamwTensor& t = tab.t[ti];
-        const bool vec = tab.vec[ti] != 0;
-        const long long base = (tile - (ti ? tab.tile_end[ti - 1] : 0)) * kTile + warp * kAdamwBlock;
-        if (base >= t.n) continue;
-        const long long blk = base / kAdamwBlock;
-        const float am = t.ms[blk], av = t.vs[blk];
-        const long long e0 = base + lane * 4;
+    for (long long tile = blockIdx.x; tile < tiles; tile += 2ll * gridDim.x) {
+        int ti[2];
+        long long base[2];
+        bool fast[2];
+        uint32_t cm[2][2], cv[2][2];
+        float am[2], av[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float m[4], v[4];
-            decode4(get_codes(t.m, e0 + j * 128, t.n, vec), get_codes(t.v, e0 + j * 128, t.n, vec), am, av, m, v);
-            put4(P.m_out[ti], e0 + j * 128, t.n, vec, m);
-            put4(P.v_out[ti], e0 + j * 128, t.n, vec, v);
+        for (int k = 0; k < 2; ++k) {
+            if (!find_piece(tab, tile + k * (long long)gridDim.x, ti[k], base[k], fast[k])) continue;
+            const AdamwTensor& t = tab.t[ti[k]];
+            am[k] = t.ms[base[k] / kAdamwBlock];
+            av[k] = t.vs[base[k] / kAdamwBlock];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const long long e = base[k] + lane * 4 + j * 128;
+                cm[k][j] = fast[k] ? get_codes<true>(t.m, e, t.n) : get_codes<false>(t.m, e, t.n);
+                cv[k][j] = fast[k] ? get_codes<true>(t.v, e, t.n) : get_codes<false>(t.v, e, t.n);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (ti[k] < 0) continue;
+            const long long n = tab.t[ti[k]].n;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const long long e = base[k] + lane * 4 + j * 128;
+                float m[4], v[4];
+                decode4(cm[k][j], cv[k][j], am[k], av[k], m, v);
+                if (fast[k]) {
+                    put4<true>(P.m_out[ti[k]], e, n, m);
+                    put4<true>(P.v_out[ti[k]], e, n, v);
+                } else {
+                    put4<false>(P.m_out[ti[k]], e, n, m);
+                    put4<false>(P.v_out[ti[k]], e, n, v);
+                }
+            }
         }
     }
 }
@@ -456,7 +506,7 @@ cudaError_t launch_adamw_read(const void* args, cudaStream_t s, int* nlaunch) {
         P.tab.vec[i] = aligned(a.t[i].m, 4) && aligned(a.t[i].v, 4) && aligned(a.m_out[i], 16) &&
                        aligned(a.v_out[i], 16);
     }
-    const int grid = (int)(tiles < (long long)a.num_sms * 8 ? tiles : (long long)a.num_sms * 8);
+    const int grid = (int)(tiles < (long long)a.num_sms * 6 ? tiles : (long long)a.num_sms * 6);
     adamw_read_kernel<<<grid, kThreads, 0, s>>>(P);
     ++*nlaunch;
     return cudaGetLastError();
