@@ -87,13 +87,14 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 // u / 2^16 ((c + 1)^2 - c^2) < X - c^2.  The root may be off by its last bits:
 // where that moves c by one, X lies within them of a code, and either start
 // leads to that code (below it, the gap to it exceeds u / 2^16 times the gap;
-// at it, nothing remains to round up).  So the largest code is not passed.
+// at it, nothing remains to round up).  So the largest code is not passed.  The
+// code is the low byte of what is returned.
 __device__ __forceinline__ uint32_t encode_m(float z, float u) {
     const float X = __fmul_rn(z, 16129.0f);
     const float f = __fadd_rd(sqrt_ftz(X), 8388608.0f);   // the whole part, in the low bits
     const float c = f - 8388608.0f;
     const float gap = fmaf(c, 0x1p-15f, 0x1p-16f);        // 2^-16 (2 c + 1), exact
-    return (__float_as_uint(f) & 255u) + (__fmul_rn(u, gap) < __fsub_rn(X, __fmul_rn(c, c)) ? 1u : 0u);
+    return __float_as_uint(f) + (__fmul_rn(u, gap) < __fsub_rn(X, __fmul_rn(c, c)) ? 1u : 0u);
 }
 // X = z 255^4 and the fourth powers.  A second moment that is not zero keeps a
 // code of at least 1: a zero under the root would let the next step divide by
@@ -104,8 +105,12 @@ __device__ __forceinline__ uint32_t encode_v(float z, float u) {
     const float c = f - 8388608.0f;
     const float lo2 = __fmul_rn(c, c), hi2 = __fadd_rn(lo2, fmaf(c, 2.0f, 1.0f));
     const float lo = __fmul_rn(lo2, lo2), gap = __fsub_rn(__fmul_rn(hi2, hi2), lo);
-    const uint32_t k = (__float_as_uint(f) & 255u) + (__fmul_rn(u * 0x1p-16f, gap) < __fsub_rn(X, lo) ? 1u : 0u);
-    return max(k, X > 0.0f ? 1u : 0u);
+    const uint32_t k = __float_as_uint(f) + (__fmul_rn(u * 0x1p-16f, gap) < __fsub_rn(X, lo) ? 1u : 0u);
+    return max(k, 0x4B000000u + min(__float_as_uint(X), 1u));   // (X is not negative)
+}
+
+__device__ __forceinline__ uint32_t low_bytes(const uint32_t (&k)[4]) {
+    return __byte_perm(__byte_perm(k[0], k[1], 0x0040u), __byte_perm(k[2], k[3], 0x0040u), 0x5410u);
 }
 
 struct Coef {
@@ -209,17 +214,6 @@ __device__ __forceinline__ void put_codes(void* p, long long e, long long n, uin
     }
 }
 
-// Tensor of tile `t`: the first whose tile_end exceeds it.
-__device__ __forceinline__ int find_tensor(const Table& tab, long long t) {
-    int lo = 0, hi = tab.count - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (tab.tile_end[mid] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
 // Largest magnitude; NaN if either is one.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -244,11 +238,15 @@ struct Piece {
     float am, av;
 };
 
-// Finds the warp's block of tile `tile`; false when there is none.
-__device__ __forceinline__ bool find_piece(const Table& tab, long long tile, int& ti, long long& base, bool& fast) {
+// Finds the warp's block of tile `tile`; false when there is none.  *at: the
+// tensor of an earlier tile (tiles come in rising order, so it only moves up).
+__device__ __forceinline__ bool find_piece(const Table& tab, long long tile, int& at, int& ti, long long& base,
+                                           bool& fast) {
     ti = -1;
     if (tile >= tab.tile_end[tab.count - 1]) return false;
-    const int i = find_tensor(tab, tile);
+    int i = at;
+    while (tab.tile_end[i] <= tile) ++i;
+    at = i;
     base = (tile - (i ? tab.tile_end[i - 1] : 0)) * kTile + (threadIdx.x >> 5) * kAdamwBlock;
     if (base >= tab.t[i].n) return false;   // (the whole warp)
     ti = i;
@@ -275,8 +273,8 @@ __device__ __forceinline__ void load_elements(const AdamwTensor& t, Piece<BITS>&
 }
 
 template <typename G, int BITS>
-__device__ __forceinline__ void load_piece(const Table& tab, long long tile, Piece<BITS>& x) {
-    if (!find_piece(tab, tile, x.ti, x.base, x.fast)) return;
+__device__ __forceinline__ void load_piece(const Table& tab, long long tile, int& at, Piece<BITS>& x) {
+    if (!find_piece(tab, tile, at, x.ti, x.base, x.fast)) return;
     const AdamwTensor& t = tab.t[x.ti];
     if (x.fast) load_elements<true, G>(t, x);
     else load_elements<false, G>(t, x);
@@ -332,7 +330,7 @@ __device__ __forceinline__ void step_piece(const Params& P, const Coef& c, const
                              (uint32_t)((unsigned long long)w.base >> 32) * 0x9E3779B9u;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            uint32_t cm = 0, cv = 0;
+            uint32_t cm[4], cv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t r = pcg((uint32_t)(e0 + j * 128 + i) ^ key);
@@ -340,11 +338,11 @@ __device__ __forceinline__ void step_piece(const Params& P, const Coef& c, const
                 const float uv = __uint_as_float(__byte_perm(r, 0x4B000000u, 0x7432u)) - 8388608.0f;
                 const uint32_t k = encode_m(fminf(__fmul_rn(fabsf(m[j][i]), im), 1.0f), um);
                 const uint32_t sign = (uint32_t)(__float_as_int(m[j][i]) >> 31);   // all ones below zero
-                cm |= (((k ^ sign) - sign) & 255u) << (8 * i);
-                cv |= encode_v(fminf(__fmul_rn(v[j][i], iv), 1.0f), uv) << (8 * i);
+                cm[i] = (k ^ sign) - sign;
+                cv[i] = encode_v(fminf(__fmul_rn(v[j][i], iv), 1.0f), uv);
             }
-            put_codes<FAST>(t.m, e0 + j * 128, n, cm);
-            put_codes<FAST>(t.v, e0 + j * 128, n, cv);
+            put_codes<FAST>(t.m, e0 + j * 128, n, low_bytes(cm));
+            put_codes<FAST>(t.v, e0 + j * 128, n, low_bytes(cv));
         }
         if (lane == 0) {
             const long long blk = w.base / kAdamwBlock;
@@ -361,14 +359,15 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 3 : 2) adamw_kernel(cons
     __shared__ Coef coef;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Piece<BITS> x;
-    load_piece<G, BITS>(P.tab, blockIdx.x, x);
+    int at = 0;
+    load_piece<G, BITS>(P.tab, blockIdx.x, at, x);
     make_coef(P, coef);
     __syncthreads();
     const Coef c = coef;
     const long long tiles = P.tab.tile_end[P.tab.count - 1];
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const Piece<BITS> w = x;
-        load_piece<G, BITS>(P.tab, tile + gridDim.x, x);
+        load_piece<G, BITS>(P.tab, tile + gridDim.x, at, x);
         if (w.ti < 0) continue;
         if (w.fast) step_piece<true>(P, c, w);
         else step_piece<false>(P, c, w);
@@ -392,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 6) adamw_read_kernel(const __grid_co
     const Table& tab = P.tab;
     const int lane = threadIdx.x & 31;
     const long long tiles = tab.tile_end[tab.count - 1];
+    int at = 0;
     for (long long tile = blockIdx.x; tile < tiles; tile += 2ll * gridDim.x) {
         int ti[2];
         long long base[2];
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 6) adamw_read_kernel(const __grid_co
         float am[2], av[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (!find_piece(tab, tile + k * (long long)gridDim.x, ti[k], base[k], fast[k])) continue;
+            if (!find_piece(tab, tile + k * (long long)gridDim.x, at, ti[k], base[k], fast[k])) continue;
             const AdamwTensor& t = tab.t[ti[k]];
             am[k] = t.ms[base[k] / kAdamwBlock];
             av[k] = t.vs[base[k] / kAdamwBlock];
