@@ -119,27 +119,28 @@ __global__ void __launch_bounds__(kThreads) norm_dx_kernel(const NormBwdArgs a) 
     }
 }
 
-// dw[c], db[c]: the groups' sums, every eighth by one of 8 warps, the warps'
-// added in order.
-__global__ void __launch_bounds__(kThreads) norm_add_kernel(const float* part, int groups, int cols, float* dw,
-                                                            float* db) {
-    __shared__ float sw[8][33], sb[8][33];
+// dw[c] (blockIdx.y 0) or db[c]: the groups' sums, every 32nd by one of 32
+// warps, the warps' added in order.  A programmatic dependent of the kernel
+// that leaves the sums.
+constexpr int kAddThreads = 1024;
+__global__ void __launch_bounds__(kAddThreads) norm_add_kernel(const float* part, int groups, int cols, float* dw,
+                                                               float* db) {
+    __shared__ float sums[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float* out = blockIdx.y ? db : dw;
+    if (!out) return;
     const int l = threadIdx.x & 31, wr = threadIdx.x >> 5, c = blockIdx.x * 32 + l;
-    float w = 0.0f, b = 0.0f;
+    float v = 0.0f;
     if (c < cols) {
-#pragma unroll 8
-        for (int g = wr; g < groups; g += 8) {
-            w += part[((size_t)g * 2 + 0) * cols + c];
-            b += part[((size_t)g * 2 + 1) * cols + c];
-        }
+#pragma unroll 4
+        for (int g = wr; g < groups; g += 32) v += part[((size_t)g * 2 + blockIdx.y) * cols + c];
     }
-    sw[wr][l] = w;
-    sb[wr][l] = b;
+    sums[wr][l] = v;
     __syncthreads();
     if (wr != 0 || c >= cols) return;
-    for (int i = 1; i < 8; ++i) { w += sw[i][l]; b += sb[i][l]; }
-    if (dw) dw[c] = w;
-    if (db) db[c] = b;
+#pragma unroll
+    for (int i = 1; i < 32; ++i) v += sums[i][l];
+    out[c] = v;
 }
 
 // ------------------------------------------------------------ rows in registers
@@ -157,58 +158,170 @@ constexpr int per_of() { return sizeof(T) == 2 && W > 1 ? 16 : 8; }
 
 constexpr int block_of(int G) { return G > kThreads ? G : kThreads; }
 
-// W consecutive elements, zeros past the row's end (c is a multiple of W, the
-// row's length too).
-template <typename T, int W>
-struct Vec {
-    uint4 q;
-    __device__ __forceinline__ void load(const T* p) { q = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-        else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-    }
-};
-template <typename T>
-struct Vec<T, 1> {
-    T q;
-    __device__ __forceinline__ void load(const T* p) { q = *p; }
-    __device__ __forceinline__ void zero() { q = from_f<T>(0.0f); }
-    __device__ __forceinline__ float get(int) const { return to_f(q); }
-};
-
-template <typename T, int W>
-__device__ __forceinline__ void store_vec(T* p, const float* v) {
-    if constexpr (W == 1) {
-        *p = from_f<T>(v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-    }
+// Two float32 values in one register pair: sm_100a adds, multiplies and fuses
+// them in one instruction, which is what keeps the arithmetic (a fifth of the
+// issue slots otherwise spent) out of HBM's way.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float a, b;
+    split(v, a, b);
+    return a + b;
 }
 
-// A group's part of a row (or of weight, bias).
+// A group's part of a row as it is stored: PER elements, loads of W.
 template <typename T, int G, int W>
 struct Part {
-    static constexpr int NV = per_of<T, W>() / W;
-    Vec<T, W> v[NV];
-    __device__ __forceinline__ void load(const T* p, int lane, int cols, bool on) {
+    static constexpr int PER = per_of<T, W>(), NV = PER / W, NP = PER / 2;
+    uint4 q[W > 1 ? NV : 1];
+    T e[W > 1 ? 1 : NV];
+
+    __device__ __forceinline__ void load(const T* p, int lane, int cols, bool on, float fill) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * G + lane) * W;
-            if (on && c < cols) v[j].load(p + c);
-            else v[j].zero();
+            const bool in = on && c < cols;
+            if constexpr (W > 1) {
+                if (in) q[j] = __ldg(reinterpret_cast<const uint4*>(p + c));
+                else if constexpr (sizeof(T) == 4) q[j] = fill_of(__float_as_uint(fill));
+                else q[j] = fill_of((__float_as_uint(fill) >> 16) * 0x10001u);
+            } else {
+                e[j] = in ? p[c] : from_f<T>(fill);
+            }
         }
     }
-    __device__ __forceinline__ float get(int i) const { return v[i / W].get(i % W); }
+    static __device__ __forceinline__ uint4 fill_of(uint32_t w) { return make_uint4(w, w, w, w); }
+    // Elements 2 i and 2 i + 1.
+    __device__ __forceinline__ f2 get(int i) const {
+        if constexpr (W == 1) {
+            return pair(to_f(e[2 * i]), to_f(e[2 * i + 1]));
+        } else if constexpr (sizeof(T) == 4) {
+            const uint4 v = q[i / 2];
+            return i & 1 ? pair(__uint_as_float(v.z), __uint_as_float(v.w)) : pair(__uint_as_float(v.x), __uint_as_float(v.y));
+        } else {
+            const uint4 v = q[i / 4];
+            const uint32_t w = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        }
+    }
+    // Stores values v where columns exist.
+    static __device__ __forceinline__ void store(T* p, int lane, int cols, const f2 (&v)[NP]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * G + lane) * W;
+            if (c >= cols) continue;
+            if constexpr (W == 1) {
+                float a, b;
+                split(v[j / 2], a, b);
+                p[c] = from_f<T>(j & 1 ? b : a);
+            } else if constexpr (sizeof(T) == 4) {
+                float4 o;
+                split(v[2 * j], o.x, o.y);
+                split(v[2 * j + 1], o.z, o.w);
+                *reinterpret_cast<float4*>(p + c) = o;
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float a, b;
+                    split(v[4 * j + i], a, b);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    // Zeros in the places past the row's end.
+    static __device__ __forceinline__ void clear(int lane, int cols, f2 (&v)[NP]) {
+        if (cols == G * PER) return;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if ((j * G + lane) * W < cols) continue;
+            if constexpr (W == 1) {
+                float a, b;
+                split(v[j / 2], a, b);
+                v[j / 2] = j & 1 ? pair(a, 0.0f) : pair(0.0f, b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) v[j * (W / 2) + i] = 0;
+            }
+        }
+    }
+};
+
+// The rows ahead of the current one, in shared memory: every thread copies
+// (cp.async) and reads back only its own part, so no barrier is involved, and
+// kAhead rows of a group are in flight without a register.  (HBM's latency
+// times an SM's share of its rate is some 50 KB; one row ahead in registers was
+// 32 KB of the forward's and a third slower.)  Rows that 16-byte copies cannot
+// take (W = 1) keep one row ahead in registers.
+constexpr int kAhead = 3;
+
+template <typename T, int G, int W, int ARRAYS>
+struct Ring {
+    static constexpr int NV = per_of<T, W>() / W, THREADS = block_of(G);
+    static constexpr size_t BYTES = W > 1 ? (size_t)(kAhead + 1) * ARRAYS * NV * THREADS * 16 : 0;
+    uint4* slots;   // [kAhead + 1][ARRAYS][NV][THREADS]
+    Part<T, G, W> next[W > 1 ? 1 : ARRAYS];
+
+    __device__ __forceinline__ uint4* slot(int stage, int a, int j) const {
+        return slots + ((stage * ARRAYS + a) * NV + j) * THREADS + threadIdx.x;
+    }
+    // Array a's part of a row, to stage `stage` (W = 1: to registers).
+    __device__ __forceinline__ void issue(int stage, int a, const T* p, int lane, int cols, bool on) {
+        if constexpr (W > 1) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * G + lane) * W;
+                if (on && c < cols)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     (uint32_t)__cvta_generic_to_shared(slot(stage, a, j))),
+                                 "l"(p + c)
+                                 : "memory");
+            }
+        } else {
+            next[a].load(p, lane, cols, on, 0.0f);
+        }
+    }
+    __device__ __forceinline__ void commit() const {
+        if constexpr (W > 1) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // All but the newest kAhead - 1 rows have landed.
+    __device__ __forceinline__ void wait() const {
+        if constexpr (W > 1) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    }
+    __device__ __forceinline__ void take(int stage, int a, int lane, int cols, Part<T, G, W>& x) const {
+        if constexpr (W > 1) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                x.q[j] = (j * G + lane) * W < cols ? *slot(stage, a, j) : make_uint4(0, 0, 0, 0);
+            }
+        } else {
+            x = next[a];
+        }
+    }
 };
 
 // Sums of N values over each group of G threads, in every thread of it.
@@ -241,53 +354,62 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) 
 
 template <typename T, int G, int W>
 __global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows_kernel(const NormFwdArgs a) {
-    constexpr int kPer = per_of<T, W>();
+    using P = Part<T, G, W>;
     constexpr int RPB = block_of(G) / G;
     __shared__ float red[2 * block_of(G) / 32];
     int flip = 0;
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
     const int C = a.cols;
     const float inv = 1.0f / (float)C;
-    Part<T, G, W> w, b, x, nx;
-    w.load(static_cast<const T*>(a.w), lane, C, a.w != nullptr);
-    b.load(static_cast<const T*>(a.b), lane, C, a.b != nullptr);
+    constexpr int kRows = W > 1 ? kAhead : 1;
+    extern __shared__ uint4 ring_slots[];
+    Ring<T, G, W, 1> ring;
+    ring.slots = ring_slots;
+    Part<T, G, W> w, b, x;
     const long long step = (long long)gridDim.x * RPB;
     long long r = (long long)blockIdx.x * RPB + grp;
     const T* X = static_cast<const T*>(a.x);
-    nx.load(X + r * C, lane, C, r < a.rows);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        ring.issue(k, 0, X + (r + k * step) * C, lane, C, r + k * step < a.rows);
+        ring.commit();
+    }
+    w.load(static_cast<const T*>(a.w), lane, C, a.w != nullptr, 1.0f);
+    b.load(static_cast<const T*>(a.b), lane, C, a.b != nullptr, 0.0f);
+    int stage = 0;
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += step, r += step) {
         const bool on = r < a.rows;
-        x = nx;
-        nx.load(X + (r + step) * C, lane, C, r + step < a.rows);
-        float s[1] = {0.0f};
+        ring.wait();
+        ring.take(stage, 0, lane, C, x);
+        // (the stage before this one: what it held has been read)
+        const int behind = stage == 0 ? kAhead : stage - 1;
+        ring.issue(behind, 0, X + (r + kRows * step) * C, lane, C, r + kRows * step < a.rows);
+        ring.commit();
+        stage = stage == kAhead ? 0 : stage + 1;
+        f2 d[P::NP], acc = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) s[0] += x.get(i);
+        for (int i = 0; i < P::NP; ++i) {
+            d[i] = x.get(i);
+            acc = add2(acc, d[i]);
+        }
+        float s[1] = {sum2(acc)};
         group_sum<G>(s, red, flip);
         const float mean = s[0] * inv;
-        s[0] = 0.0f;
+        const f2 minus = both(-mean);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = ((i / W) * G + lane) * W;
-            const float d = x.get(i) - mean;
-            if (c < C) s[0] = fmaf(d, d, s[0]);
-        }
+        for (int i = 0; i < P::NP; ++i) d[i] = add2(d[i], minus);
+        P::clear(lane, C, d);
+        acc = 0;
+#pragma unroll
+        for (int i = 0; i < P::NP; ++i) acc = fma2(d[i], d[i], acc);
+        s[0] = sum2(acc);
         group_sum<G>(s, red, flip);
         const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
         if (on) {
-            T* y = static_cast<T*>(a.y) + r * C;
+            const f2 scale = both(rstd);
 #pragma unroll
-            for (int j = 0; j < kPer / W; ++j) {
-                const int c = (j * G + lane) * W;
-                if (c >= C) continue;
-                float o[W];
-#pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    o[i] = (x.get(j * W + i) - mean) * rstd;
-                    if (a.w) o[i] *= w.get(j * W + i);
-                    if (a.b) o[i] += b.get(j * W + i);
-                }
-                store_vec<T, W>(y + c, o);
-            }
+            for (int i = 0; i < P::NP; ++i) d[i] = fma2(mul2(d[i], scale), w.get(i), b.get(i));
+            P::store(static_cast<T*>(a.y) + r * C, lane, C, d);
             if (lane == 0) {
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
@@ -300,6 +422,7 @@ __global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows
 // sums of its own 16 columns in registers, the groups are added at the end.
 template <typename T, int G, int W>
 __global__ void __launch_bounds__(block_of(G), 512 / block_of(G)) norm_bwd_rows_kernel(const NormBwdArgs a) {
+    using P = Part<T, G, W>;
     constexpr int kPer = per_of<T, W>();
     constexpr int RPB = block_of(G) / G;
     __shared__ float red[4 * block_of(G) / 32];
@@ -309,65 +432,72 @@ __global__ void __launch_bounds__(block_of(G), 512 / block_of(G)) norm_bwd_rows_
     const int C = a.cols;
     const float inv = 1.0f / (float)C;
     const bool sums = a.dw != nullptr || a.db != nullptr;
-    Part<T, G, W> w, x, g, nx, ng;
-    w.load(static_cast<const T*>(a.w), lane, C, a.w != nullptr);
-    float dw[kPer] = {}, db[kPer] = {};
+    constexpr int kRows = W > 1 ? kAhead : 1;
+    extern __shared__ uint4 ring_slots[];
+    Ring<T, G, W, 2> ring;
+    ring.slots = ring_slots;
+    Part<T, G, W> w, x, g;
+    f2 dw[P::NP] = {}, db[P::NP] = {};
     const long long step = (long long)gridDim.x * RPB;
     long long r = (long long)blockIdx.x * RPB + grp;
     const T* X = static_cast<const T*>(a.x);
     const T* Y = static_cast<const T*>(a.gy);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        ring.issue(k, 0, X + (r + k * step) * C, lane, C, r + k * step < a.rows);
+        ring.issue(k, 1, Y + (r + k * step) * C, lane, C, r + k * step < a.rows);
+        ring.commit();
+    }
+    w.load(static_cast<const T*>(a.w), lane, C, a.w != nullptr, 1.0f);
     float nmean = 0.0f, nrstd = 0.0f;
-    nx.load(X + r * C, lane, C, r < a.rows);
-    ng.load(Y + r * C, lane, C, r < a.rows);
     if (r < a.rows) { nmean = a.mean[r]; nrstd = a.rstd[r]; }
+    int stage = 0;
     for (long long r0 = (long long)blockIdx.x * RPB; r0 < a.rows; r0 += step, r += step) {
         const bool on = r < a.rows;
-        x = nx; g = ng;
         const float mean = nmean, rstd = nrstd;
-        const bool more = r + step < a.rows;
-        nx.load(X + (r + step) * C, lane, C, more);
-        ng.load(Y + (r + step) * C, lane, C, more);
-        if (more) { nmean = a.mean[r + step]; nrstd = a.rstd[r + step]; }
-        float s[2] = {0.0f, 0.0f};
-        if (on) {   // past the last row there is nothing to sum (0 times a stale mean could be NaN)
+        if (r + step < a.rows) { nmean = a.mean[r + step]; nrstd = a.rstd[r + step]; }
+        ring.wait();
+        ring.take(stage, 0, lane, C, x);
+        ring.take(stage, 1, lane, C, g);
+        const int behind = stage == 0 ? kAhead : stage - 1;
+        const bool more = r + kRows * step < a.rows;
+        ring.issue(behind, 0, X + (r + kRows * step) * C, lane, C, more);
+        ring.issue(behind, 1, Y + (r + kRows * step) * C, lane, C, more);
+        ring.commit();
+        stage = stage == kAhead ? 0 : stage + 1;
+        f2 xh[P::NP], gw[P::NP], s1 = 0, s2 = 0;
+        const f2 scale = both(rstd), minus = both(-mean);
+        if (on) {   // past the last row there is nothing to sum
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int c = ((i / W) * G + lane) * W;
-                const float gy = g.get(i), xh = (x.get(i) - mean) * rstd;
-                if (c < C) {
-                    dw[i] = fmaf(gy, xh, dw[i]);
-                    db[i] += gy;
-                    const float gw = a.w ? gy * w.get(i) : gy;
-                    s[0] += gw;
-                    s[1] = fmaf(gw, xh, s[1]);
-                }
+            for (int i = 0; i < P::NP; ++i) {
+                const f2 gy = g.get(i);
+                xh[i] = mul2(add2(x.get(i), minus), scale);
+                dw[i] = fma2(gy, xh[i], dw[i]);
+                db[i] = add2(db[i], gy);
+                gw[i] = mul2(gy, w.get(i));
+                s1 = add2(s1, gw[i]);
+                s2 = fma2(gw[i], xh[i], s2);
             }
         }
         if (a.dx) {
+            float s[2] = {sum2(s1), sum2(s2)};
             group_sum<G>(s, red, flip);
-            const float s1 = s[0] * inv, s2 = s[1] * inv;
             if (on) {
-                T* dx = static_cast<T*>(a.dx) + r * C;
+                const f2 m1 = both(-s[0] * inv), m2 = both(-s[1] * inv);
 #pragma unroll
-                for (int j = 0; j < kPer / W; ++j) {
-                    const int c = (j * G + lane) * W;
-                    if (c >= C) continue;
-                    float o[W];
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const float gy = g.get(j * W + i), xh = (x.get(j * W + i) - mean) * rstd;
-                        o[i] = rstd * ((a.w ? gy * w.get(j * W + i) : gy) - s1 - xh * s2);
-                    }
-                    store_vec<T, W>(dx + c, o);
-                }
+                for (int i = 0; i < P::NP; ++i) gw[i] = mul2(scale, fma2(xh[i], m2, add2(gw[i], m1)));
+                P::store(static_cast<T*>(a.dx) + r * C, lane, C, gw);
             }
         }
     }
     if (!sums) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // norm_add_kernel sets off
     float* out = a.part + (size_t)blockIdx.x * 2 * C;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        float* v = k ? db : dw;
+        float v[kPer];
+#pragma unroll
+        for (int i = 0; i < P::NP; ++i) split(k ? db[i] : dw[i], v[2 * i], v[2 * i + 1]);
         if constexpr (RPB > 1) {
             __syncthreads();
 #pragma unroll
@@ -436,7 +566,10 @@ template <typename T, int W>
 bool fwd_rows(const NormFwdArgs& a, cudaStream_t s) {
     return with_group(group_of(a.cols, per_of<T, W>()), [&](auto g) {
         constexpr int G = decltype(g)::value;
-        norm_fwd_rows_kernel<T, G, W><<<(int)row_blocks(a.rows, G, kFwdThreads, a.num_sms), block_of(G), 0, s>>>(a);
+        constexpr size_t bytes = Ring<T, G, W, 1>::BYTES;
+        if (bytes > 16 * 1024)   // with the static part it may pass 48 KB
+            cudaFuncSetAttribute(norm_fwd_rows_kernel<T, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        norm_fwd_rows_kernel<T, G, W><<<(int)row_blocks(a.rows, G, kFwdThreads, a.num_sms), block_of(G), bytes, s>>>(a);
     });
 }
 
@@ -446,7 +579,10 @@ bool bwd_rows(const NormBwdArgs& a, cudaStream_t s, int* groups) {
     return with_group(group_of(a.cols, per_of<T, W>()), [&](auto g) {
         constexpr int G = decltype(g)::value;
         *groups = (int)row_blocks(a.rows, G, kBwdThreads, a.num_sms);
-        norm_bwd_rows_kernel<T, G, W><<<*groups, block_of(G), 0, s>>>(a);
+        constexpr size_t bytes = Ring<T, G, W, 2>::BYTES;
+        if (bytes > 16 * 1024)   // with the static part it may pass 48 KB
+            cudaFuncSetAttribute(norm_bwd_rows_kernel<T, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        norm_bwd_rows_kernel<T, G, W><<<*groups, block_of(G), bytes, s>>>(a);
     });
 }
 
@@ -480,9 +616,18 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s, int* n) {
             ++*n;
             if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
-        norm_add_kernel<<<(a.cols + 31) / 32, kThreads, 0, s>>>(a.part, groups, a.cols, a.dw, a.db);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((a.cols + 31) / 32, 2);
+        cfg.blockDim = dim3(kAddThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, norm_add_kernel, (const float*)a.part, groups, a.cols, a.dw, a.db);
         ++*n;
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
     }
     if (a.dx && a.rows > 0 && !rows) {
         const long long grid = a.rows < 8ll * a.num_sms ? a.rows : 8ll * a.num_sms;
