@@ -25,7 +25,8 @@ constexpr int kThreads = 256;
 
 template <int D>
 constexpr size_t smem_floats() {
-    return (size_t)3 * C * (D + 4) + (size_t)D * (D + 4) + (size_t)C * (C + 4) + C + 1;
+    // a (the scores over it), b, c, X, powers
+    return (size_t)C * (D + 4 > C + 4 ? D + 4 : C + 4) + (size_t)2 * C * (D + 4) + (size_t)D * (D + 4) + C + 1;
 }
 
 // N consecutive floats of shared memory (N = 2 or a multiple of 4).
@@ -68,17 +69,17 @@ __device__ __forceinline__ bool can_vec(const void* p, long long ld, int d) {
 
 // MODE: see LinMode.
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kThreads) lin_kernel(const __grid_constant__ LinArgs g) {
+__global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const __grid_constant__ LinArgs g) {
     constexpr int P = D + 4, PC = C + 4;
     constexpr int W = D / 16 < 4 ? D / 16 : 4;   // consecutive columns of a thread's tile
     constexpr int NW = D / 16 / W;               // tiles of W columns, 16 W apart
     extern __shared__ float sm[];
     float* sa = sm;
-    float* sb = sa + C * P;
+    float* sp = sm;            // the scores, once a has been read: three blocks of D = 64 share an SM
+    float* sb = sa + C * (P > PC ? P : PC);
     float* sc = sb + C * P;
     float* sx = sc + C * P;
-    float* sp = sx + D * P;
-    float* gp = sp + C * PC;   // g^0 .. g^C
+    float* gp = sx + D * P;    // g^0 .. g^C
 
     if (MODE != kLinSegments && blockIdx.x == 0 && threadIdx.x == 0) *g.status = kStatusOk;
     LinItem it;
@@ -108,9 +109,11 @@ __global__ void __launch_bounds__(kThreads) lin_kernel(const __grid_constant__ L
         load_chunk<T, D>(sc, c, row, tau, m, J.ldc, J.dc, vc);
         __syncthreads();
         if (MODE != kLinStates) {
-            // scores of rows ty*4 + i, columns tx + 16 j
+            // scores of rows ty*4 + i, columns tx + 16 j, and a X
             float p[4][4] = {};
+            float acc[4][NW][W] = {};
             if (ty * 4 < m) {
+#pragma unroll 2
                 for (int k = 0; k < da4; k += 4) {
                     float x[4][4], y[4][4];
 #pragma unroll
@@ -124,8 +127,20 @@ __global__ void __launch_bounds__(kThreads) lin_kernel(const __grid_constant__ L
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) p[i][j] = fmaf(x[i][q], y[j][q], p[i][j]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int u = 0; u < NW; ++u) {
+                            float z[W];
+                            lds<W>(sx + (k + q) * P + u * 16 * W + tx * W, z);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int j = 0; j < W; ++j) acc[i][u][j] = fmaf(x[i][q], z[j], acc[i][u][j]);
+                        }
                 }
             }
+            __syncthreads();   // a has been read
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -134,24 +149,7 @@ __global__ void __launch_bounds__(kThreads) lin_kernel(const __grid_constant__ L
                     sp[r * PC + q] = q <= r ? p[i][j] * (gp[r - q] * J.bscale) : 0.0f;
                 }
             __syncthreads();
-            float acc[4][NW][W] = {};
             if (ty * 4 < m) {
-                for (int k = 0; k < da4; k += 4) {
-                    float x[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) lds<4>(sa + (ty * 4 + i) * P + k, x[i]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int u = 0; u < NW; ++u) {
-                            float y[W];
-                            lds<W>(sx + (k + q) * P + u * 16 * W + tx * W, y);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int j = 0; j < W; ++j) acc[i][u][j] = fmaf(x[i][q], y[j], acc[i][u][j]);
-                        }
-                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float f = gp[ty * 4 + i + it.e];
