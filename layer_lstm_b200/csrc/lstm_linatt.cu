@@ -48,11 +48,30 @@ __device__ __forceinline__ void load_chunk(float* dst, const T* src, const LinRo
                                            int d, bool vec) {
     constexpr int P = D + 4;
     if (vec) {
-        for (int i = threadIdx.x; i < C * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < m && c < d) load4(src + row.at(tau0 + r) * ld + c, v);
-            *reinterpret_cast<float4*>(dst + r * P + c) = make_float4(v[0], v[1], v[2], v[3]);
+        // all of a thread's loads in flight at once (float32: straight to
+        // shared memory, awaited by chunk_landed)
+        constexpr int NL = C * (D / 4) / kThreads;
+        float v[NL][4];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int i = threadIdx.x + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+            const bool in = r < m && c < d;
+            if constexpr (sizeof(T) == 4) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(dst + r * P + c)),
+                             "l"(in ? src + row.at(tau0 + r) * ld + c : src), "r"(in ? 16 : 0)
+                             : "memory");
+            } else {
+                v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0.0f;
+                if (in) load4(src + row.at(tau0 + r) * ld + c, v[j]);
+            }
+        }
+        if constexpr (sizeof(T) != 4) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int i = threadIdx.x + j * kThreads, r = i / (D / 4), c = (i % (D / 4)) * 4;
+                *reinterpret_cast<float4*>(dst + r * P + c) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+            }
         }
     } else {
         for (int i = threadIdx.x; i < C * D; i += kThreads) {
@@ -61,6 +80,8 @@ __device__ __forceinline__ void load_chunk(float* dst, const T* src, const LinRo
         }
     }
 }
+
+__device__ __forceinline__ void chunk_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T>
 __device__ __forceinline__ bool can_vec(const void* p, long long ld, int d) {
@@ -107,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
         if (MODE != kLinStates) load_chunk<T, D>(sa, a, row, tau, m, J.lda, J.da, va);
         load_chunk<T, D>(sb, b, row, tau, m, J.ldb, J.da, vb);
         load_chunk<T, D>(sc, c, row, tau, m, J.ldc, J.dc, vc);
+        chunk_landed();
         __syncthreads();
         if (MODE != kLinStates) {
             // scores of rows ty*4 + i, columns tx + 16 j, and a X
