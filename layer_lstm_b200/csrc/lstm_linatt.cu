@@ -380,15 +380,17 @@ cudaError_t step_type(const LinStepArgs& a, cudaStream_t s) {
 }  // namespace
 
 int lin_segments(int B, int T, int H, int njobs, int num_sms, bool tc, int* seg_len) {
-    // Where rows, heads and products leave SMs idle: two blocks for every SM
-    // (one of the tensor-core kernel's); a segment is at least four chunks
-    // (two), since its state is written, carried and read again.
+    // Where rows, heads and products leave SMs idle, the time axis is shared
+    // out: up to two blocks for every SM (one of the tensor-core kernel's), a
+    // chunk each at least.  A segment's own state costs some 0.6 of its
+    // outputs' time, and the two launches more 6 us; a chunk takes 2 us on the
+    // tensor cores, 6 to 16 on the CUDA cores, so it pays from 6 and 3 chunks.
     const long long have = (long long)B * H * njobs;
-    const int chunk = tc ? kLinTcChunk : C, least = tc ? 2 : 4;
+    const int chunk = tc ? kLinTcChunk : C, from = tc ? 6 : 3;
     const long long want = tc ? num_sms : 2ll * num_sms;
     const int chunks = (int)(((long long)T + chunk - 1) / chunk);
     int n = 1;
-    if (have > 0 && have * 2 <= want) n = (int)std::min<long long>(want / have, chunks / least);
+    if (have > 0 && have * 2 <= want && chunks >= from) n = (int)std::min<long long>(want / have, chunks);
     if (n < 1) n = 1;
     const int per = std::max(1, (chunks + n - 1) / n);
     *seg_len = per * chunk;
