@@ -279,13 +279,19 @@ lstm_status lstm_noalloc_query_status(cudaStream_t stream);
  *   ds0 = g dS_1.
  * dq, dk, dv are required and overwritten.
  * Products are summed in float32 and the states are float32; out, dq, dk and
- * dv are rounded once.  In bf16 the scores and the state are rounded to bf16
- * as operands of the tensor cores where the key and value sizes allow them.
+ * dv are rounded once.  In bf16, key and value sizes that are multiples of 16
+ * (with 16-byte aligned arrays, rows in multiples of 8 elements, and heads *
+ * size at least 64) run on the tensor cores: there the scores and the state
+ * are rounded to bf16 as operands of out's products (not of the state's), and
+ * a decay below e^-40 acts as e^-40 in out.  Everything else runs on the CUDA
+ * cores in float32.
  * A NaN or an infinity in a step's inputs may reach the outputs of earlier
  * steps of the same chunk of up to 128.
  * Sizes from 1 to 128 for key_size and value_size; larger ones return
  * LSTM_ERR_UNSUPPORTED.  Workspace (256-byte aligned) from the query; it
- * serves forward and backward.
+ * serves forward and backward, is filled and read within a call, and holds
+ * the call's status word (lstm_query_status).  Beyond s_n over s0, no output
+ * may overlap an input or another output.
  */
 typedef struct {
     int batch;        /* >= 0 */
@@ -418,7 +424,9 @@ lstm_status lstm_adamw_read_state(const lstm_adamw_desc* desc, const long long* 
                                   float* const* m_out, float* const* v_out, cudaStream_t stream);
 
 /* Synchronises `stream` and returns the kernel-side status recorded in
- * `workspace` by the last call that used it (LSTM_OK or LSTM_ERR_TIMEOUT), or
+ * `workspace` by the last LSTM or linear-attention call (forward or backward)
+ * that used it (LSTM_OK or LSTM_ERR_TIMEOUT; the kernels of the other
+ * operators wait for nothing and record none), or
  * LSTM_ERR_CUDA if the stream reports an error.  A kernel's inter-block or
  * barrier wait gives up after 2 s, or after LSTM_B200_WAIT_TIMEOUT_NS
  * nanoseconds when that environment variable is set (read once per
