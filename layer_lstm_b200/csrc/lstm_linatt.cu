@@ -276,11 +276,19 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
     for (int i = blockIdx.y * kThreads + threadIdx.x; i < n; i += gridDim.y * kThreads) {
         float x = 0.0f;
         if (J.init) x = J.init[(size_t)bh * n + (J.init_t ? (i % J.dc) * J.da + i / J.dc : i)];
-        for (int s = 0; s < g.nseg; ++s) {
-            const float own = buf[(size_t)s * n + i];
-            buf[(size_t)s * n + i] = x;
-            const int m = lin_steps(g, len, s, J.reverse);
-            x = fmaf(expf(ld * (float)m), x, own);
+        // eight segments' states at a time: a load behind each store would
+        // cost its latency for every segment
+        constexpr int AT = 8;
+        for (int s0 = 0; s0 < g.nseg; s0 += AT) {
+            float own[AT];
+#pragma unroll
+            for (int k = 0; k < AT; ++k) own[k] = s0 + k < g.nseg ? buf[(size_t)(s0 + k) * n + i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < AT; ++k) {
+                if (s0 + k >= g.nseg) break;
+                buf[(size_t)(s0 + k) * n + i] = x;
+                x = fmaf(expf(ld * (float)lin_steps(g, len, s0 + k, J.reverse)), x, own[k]);
+            }
         }
         if (J.fin) J.fin[(size_t)bh * n + i] = x;
     }
