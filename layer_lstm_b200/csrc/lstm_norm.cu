@@ -146,16 +146,17 @@ __global__ void __launch_bounds__(kAddThreads) norm_add_kernel(const float* part
 // ------------------------------------------------------------ rows in registers
 // A row is held by a group of G threads, PER values each, and read once: W
 // consecutive values per load (16 bytes, or 1 where rows are not 16-byte
-// multiples), loads G * W columns apart.  PER is 16 for packed bf16 and 8
-// otherwise: the backward keeps two rows' x and grad_y and two column sums
-// in registers, 120 a thread, so that two blocks of 256 share an SM (with 16
-// float32 values it takes 165, one block).  A block of
-// at least 256 threads takes 256 / G rows at a time and walks the rows with
-// the next row's loads issued before the current row's sums, which is what
-// keeps HBM busy across the two reductions; weight and bias stay in registers.
+// multiples), loads G * W columns apart.  PER is 64
+// bytes of packed elements (8 elements otherwise): what a row costs beside its
+// elements, some 120 instructions of sums over the group, root and addresses,
+// is then a third of it.  (With 32 bytes, 8192 x 2048 bf16 forward and backward
+// took 47 us instead of 40.)  The backward keeps a row and two column sums in
+// registers, one block of 256 an SM; the forward two.  A block of at least 256
+// threads takes 256 / G rows at a time.
 template <typename T, int W>
-constexpr int per_of() { return sizeof(T) == 2 && W > 1 ? 16 : 8; }
+constexpr int per_of() { return W == 1 ? 8 : sizeof(T) == 2 ? 32 : 16; }
 
+constexpr int kFwdThreads = 512, kBwdThreads = 256;   // per SM, with their registers
 constexpr int block_of(int G) { return G > kThreads ? G : kThreads; }
 
 // Two float32 values in one register pair: sm_100a adds, multiplies and fuses
@@ -191,9 +192,9 @@ __device__ __forceinline__ float sum2(f2 v) {
 }
 
 // A group's part of a row as it is stored: PER elements, loads of W.
-template <typename T, int G, int W>
+template <typename T, int G, int W, int PER>
 struct Part {
-    static constexpr int PER = per_of<T, W>(), NV = PER / W, NP = PER / 2;
+    static constexpr int NV = PER / W, NP = PER / 2;
     uint4 q[W > 1 ? NV : 1];
     T e[W > 1 ? 1 : NV];
 
@@ -273,18 +274,18 @@ struct Part {
 
 // The rows ahead of the current one, in shared memory: every thread copies
 // (cp.async) and reads back only its own part, so no barrier is involved, and
-// kAhead rows of a group are in flight without a register.  (HBM's latency
-// times an SM's share of its rate is some 50 KB; one row ahead in registers was
-// 32 KB of the forward's and a third slower.)  Rows that 16-byte copies cannot
-// take (W = 1) keep one row ahead in registers.
-constexpr int kAhead = 3;
+// three rows of a group (one of the widest, by shared memory's size) are in
+// flight without a register.  (HBM's latency times an SM's share of its rate is
+// some 50 KB.)  Rows that 16-byte copies cannot take (W = 1) keep one row ahead
+// in registers.
+constexpr int ahead_of(int G) { return G > kThreads ? 1 : 3; }
 
-template <typename T, int G, int W, int ARRAYS>
+template <typename T, int G, int W, int PER, int ARRAYS>
 struct Ring {
-    static constexpr int NV = per_of<T, W>() / W, THREADS = block_of(G);
-    static constexpr size_t BYTES = W > 1 ? (size_t)(kAhead + 1) * ARRAYS * NV * THREADS * 16 : 0;
-    uint4* slots;   // [kAhead + 1][ARRAYS][NV][THREADS]
-    Part<T, G, W> next[W > 1 ? 1 : ARRAYS];
+    static constexpr int NV = PER / W, THREADS = block_of(G), AHEAD = ahead_of(G);
+    static constexpr size_t BYTES = W > 1 ? (size_t)(AHEAD + 1) * ARRAYS * NV * THREADS * 16 : 0;
+    uint4* slots;   // [AHEAD + 1][ARRAYS][NV][THREADS]
+    Part<T, G, W, PER> next[W > 1 ? 1 : ARRAYS];
 
     __device__ __forceinline__ uint4* slot(int stage, int a, int j) const {
         return slots + ((stage * ARRAYS + a) * NV + j) * THREADS + threadIdx.x;
@@ -308,11 +309,11 @@ struct Ring {
     __device__ __forceinline__ void commit() const {
         if constexpr (W > 1) asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    // All but the newest kAhead - 1 rows have landed.
+    // All but the newest AHEAD - 1 rows have landed.
     __device__ __forceinline__ void wait() const {
-        if constexpr (W > 1) asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        if constexpr (W > 1) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
     }
-    __device__ __forceinline__ void take(int stage, int a, int lane, int cols, Part<T, G, W>& x) const {
+    __device__ __forceinline__ void take(int stage, int a, int lane, int cols, Part<T, G, W, PER>& x) const {
         if constexpr (W > 1) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
@@ -353,19 +354,20 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) 
 }
 
 template <typename T, int G, int W>
-__global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows_kernel(const NormFwdArgs a) {
-    using P = Part<T, G, W>;
+__global__ void __launch_bounds__(block_of(G), kFwdThreads / block_of(G)) norm_fwd_rows_kernel(const NormFwdArgs a) {
+    constexpr int PER = per_of<T, W>();
+    using P = Part<T, G, W, PER>;
     constexpr int RPB = block_of(G) / G;
     __shared__ float red[2 * block_of(G) / 32];
     int flip = 0;
     const int lane = threadIdx.x % G, grp = threadIdx.x / G;
     const int C = a.cols;
     const float inv = 1.0f / (float)C;
-    constexpr int kRows = W > 1 ? kAhead : 1;
+    constexpr int AHEAD = ahead_of(G), kRows = W > 1 ? AHEAD : 1;
     extern __shared__ uint4 ring_slots[];
-    Ring<T, G, W, 1> ring;
+    Ring<T, G, W, PER, 1> ring;
     ring.slots = ring_slots;
-    Part<T, G, W> w, b, x;
+    P w, b, x;
     const long long step = (long long)gridDim.x * RPB;
     long long r = (long long)blockIdx.x * RPB + grp;
     const T* X = static_cast<const T*>(a.x);
@@ -382,10 +384,10 @@ __global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows
         ring.wait();
         ring.take(stage, 0, lane, C, x);
         // (the stage before this one: what it held has been read)
-        const int behind = stage == 0 ? kAhead : stage - 1;
+        const int behind = stage == 0 ? AHEAD : stage - 1;
         ring.issue(behind, 0, X + (r + kRows * step) * C, lane, C, r + kRows * step < a.rows);
         ring.commit();
-        stage = stage == kAhead ? 0 : stage + 1;
+        stage = stage == AHEAD ? 0 : stage + 1;
         f2 d[P::NP], acc = 0;
 #pragma unroll
         for (int i = 0; i < P::NP; ++i) {
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows
         for (int i = 0; i < P::NP; ++i) acc = fma2(d[i], d[i], acc);
         s[0] = sum2(acc);
         group_sum<G>(s, red, flip);
-        const float rstd = 1.0f / sqrtf(s[0] * inv + a.eps);
+        const float rstd = rsqrtf(s[0] * inv + a.eps);
         if (on) {
             const f2 scale = both(rstd);
 #pragma unroll
@@ -421,9 +423,9 @@ __global__ void __launch_bounds__(block_of(G), 1024 / block_of(G)) norm_fwd_rows
 // dx, and the block's sums of dw and db over its rows: every thread keeps the
 // sums of its own 16 columns in registers, the groups are added at the end.
 template <typename T, int G, int W>
-__global__ void __launch_bounds__(block_of(G), 512 / block_of(G)) norm_bwd_rows_kernel(const NormBwdArgs a) {
-    using P = Part<T, G, W>;
+__global__ void __launch_bounds__(block_of(G), 1) norm_bwd_rows_kernel(const NormBwdArgs a) {
     constexpr int kPer = per_of<T, W>();
+    using P = Part<T, G, W, kPer>;
     constexpr int RPB = block_of(G) / G;
     __shared__ float red[4 * block_of(G) / 32];
     __shared__ float part[RPB > 1 ? kPer * block_of(G) : 1];
@@ -432,11 +434,11 @@ __global__ void __launch_bounds__(block_of(G), 512 / block_of(G)) norm_bwd_rows_
     const int C = a.cols;
     const float inv = 1.0f / (float)C;
     const bool sums = a.dw != nullptr || a.db != nullptr;
-    constexpr int kRows = W > 1 ? kAhead : 1;
+    constexpr int AHEAD = ahead_of(G), kRows = W > 1 ? AHEAD : 1;
     extern __shared__ uint4 ring_slots[];
-    Ring<T, G, W, 2> ring;
+    Ring<T, G, W, kPer, 2> ring;
     ring.slots = ring_slots;
-    Part<T, G, W> w, x, g;
+    P w, x, g;
     f2 dw[P::NP] = {}, db[P::NP] = {};
     const long long step = (long long)gridDim.x * RPB;
     long long r = (long long)blockIdx.x * RPB + grp;
@@ -459,12 +461,12 @@ __global__ void __launch_bounds__(block_of(G), 512 / block_of(G)) norm_bwd_rows_
         ring.wait();
         ring.take(stage, 0, lane, C, x);
         ring.take(stage, 1, lane, C, g);
-        const int behind = stage == 0 ? kAhead : stage - 1;
+        const int behind = stage == 0 ? AHEAD : stage - 1;
         const bool more = r + kRows * step < a.rows;
         ring.issue(behind, 0, X + (r + kRows * step) * C, lane, C, more);
         ring.issue(behind, 1, Y + (r + kRows * step) * C, lane, C, more);
         ring.commit();
-        stage = stage == kAhead ? 0 : stage + 1;
+        stage = stage == AHEAD ? 0 : stage + 1;
         f2 xh[P::NP], gw[P::NP], s1 = 0, s2 = 0;
         const f2 scale = both(rstd), minus = both(-mean);
         if (on) {   // past the last row there is nothing to sum
@@ -530,13 +532,12 @@ int group_of(int cols, int per) {
     return 0;
 }
 
-// Blocks for `rows` rows: enough threads on every SM for `threads` of them.
+// Blocks for `rows` rows: at most `threads` threads (one block) on every SM.
 long long row_blocks(long long rows, int group, int threads, int num_sms) {
     const int rpb = block_of(group) / group;
-    const long long need = (rows + rpb - 1) / rpb, most = (long long)(threads / block_of(group)) * num_sms;
+    const long long need = (rows + rpb - 1) / rpb, most = (long long)(threads >= block_of(group) ? threads / block_of(group) : 1) * num_sms;
     return need < most ? need : most;
 }
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;   // per SM, as the launch bounds say
 
 template <typename F>
 bool with_group(int group, F&& f) {
@@ -566,7 +567,7 @@ template <typename T, int W>
 bool fwd_rows(const NormFwdArgs& a, cudaStream_t s) {
     return with_group(group_of(a.cols, per_of<T, W>()), [&](auto g) {
         constexpr int G = decltype(g)::value;
-        constexpr size_t bytes = Ring<T, G, W, 1>::BYTES;
+        constexpr size_t bytes = Ring<T, G, W, per_of<T, W>(), 1>::BYTES;
         if (bytes > 16 * 1024)   // with the static part it may pass 48 KB
             cudaFuncSetAttribute(norm_fwd_rows_kernel<T, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         norm_fwd_rows_kernel<T, G, W><<<(int)row_blocks(a.rows, G, kFwdThreads, a.num_sms), block_of(G), bytes, s>>>(a);
@@ -579,7 +580,7 @@ bool bwd_rows(const NormBwdArgs& a, cudaStream_t s, int* groups) {
     return with_group(group_of(a.cols, per_of<T, W>()), [&](auto g) {
         constexpr int G = decltype(g)::value;
         *groups = (int)row_blocks(a.rows, G, kBwdThreads, a.num_sms);
-        constexpr size_t bytes = Ring<T, G, W, 2>::BYTES;
+        constexpr size_t bytes = Ring<T, G, W, per_of<T, W>(), 2>::BYTES;
         if (bytes > 16 * 1024)   // with the static part it may pass 48 KB
             cudaFuncSetAttribute(norm_bwd_rows_kernel<T, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         norm_bwd_rows_kernel<T, G, W><<<*groups, block_of(G), bytes, s>>>(a);
@@ -644,7 +645,7 @@ int norm_partials(long long rows, int cols, int num_sms) {
     // the most that any of the backward's kernels leaves for this size; which
     // one runs depends on the pointers too
     long long n = rows < num_sms ? rows : num_sms;
-    for (int per : {8, 16}) {
+    for (int per : {8, 16, 32}) {
         const int g = group_of(cols, per);
         if (g == 0) continue;
         const long long r = row_blocks(rows, g, kBwdThreads, num_sms);
