@@ -303,3 +303,48 @@ def test_gradients_against_differences(cuda_lib):
     want = sum(p.sum().item() for p in parts)
     size = sum(p.abs().sum().item() for p in parts)
     assert abs((loss(1e-2) - loss(-1e-2)) / 2e-2 - want) <= 1e-3 * size
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (48, 80), (16, 32), (128, 128), (20, 36)])
+def test_heads_and_rows_do_not_mix(dk, dv, dt, cuda_lib):
+    """NaN in one head of one row leaves every other head and row as it is, bit for bit."""
+    B, T, H = 3, 150, 4
+    t = _inputs(B, T, H, dk, dv, dt, 15, False)
+    d = _desc(t, B, T, H, dk, dv, dt)
+    clean = _run(t, d, dt)
+    for x in ("q", "k", "v", "go"):
+        t[x][1, :, 2] = float("nan")
+    t["s0"][1, 2] = float("nan")
+    got = _run(t, d, dt)
+    keep = torch.ones(B, H, dtype=torch.bool, device="cuda")
+    keep[1, 2] = False
+    for name, a, b in zip(("out", "s_n", "dq", "dk", "dv", "ds0"), clean, got):
+        if name not in ("s_n", "ds0"):
+            a, b = a.transpose(1, 2), b.transpose(1, 2)
+        assert torch.equal(a[keep], b[keep]), name
+        assert b[1, 2].isnan().any(), name
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_other_stream_and_guard_bytes(dt, cuda_lib):
+    """A call on a stream of its own; what lies around the outputs stays."""
+    B, T, H, dk, dv = 2, 200, 2, 64, 64
+    t = _inputs(B, T, H, dk, dv, dt, 16, True)
+    d = _desc(t, B, T, H, dk, dv, dt)
+    want = _run(t, d, dt)
+    s = torch.cuda.Stream()
+    pad = 512
+    bufs = [torch.full((x.numel() + 2 * pad,), 3.0, device="cuda", dtype=x.dtype) for x in want]
+    o = [b[pad:-pad].view(x.shape) for b, x in zip(bufs, want)]
+    ws = torch.empty(binding.lstm_linear_attention_workspace_size(d), device="cuda", dtype=torch.uint8)
+    torch.cuda.synchronize()
+    binding.check(binding.lstm_linear_attention_forward(d, t["q"], t["k"], t["v"], t["ld"], t["s0"], o[0], o[1], ws,
+                                                        lengths=t["lengths"], stream=s))
+    binding.check(binding.lstm_linear_attention_backward(d, t["q"], t["k"], t["v"], t["ld"], t["s0"], t["go"],
+                                                         t["gs"], o[2], o[3], o[4], o[5], ws, lengths=t["lengths"],
+                                                         stream=s))
+    s.synchronize()
+    for x, y, b in zip(want, o, bufs):
+        assert torch.equal(x, y)
+        assert (b[:pad] == 3.0).all() and (b[-pad:] == 3.0).all()

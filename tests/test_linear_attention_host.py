@@ -44,13 +44,13 @@ def test_refused_descriptions(kw):
         assert call(d) == binding.LSTM_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(key_size=129), dict(value_size=200)])
+@pytest.mark.parametrize("kw", [dict(key_size=129), dict(value_size=200), dict(seq_len=(1 << 30) + 1)])
 def test_unsupported_sizes(kw):
     args = dict(batch=2, seq_len=1, heads=2, key_size=8, value_size=8)
     args.update(kw)
     d = binding.make_attention_desc(**args)
     assert binding.lstm_linear_attention_workspace_size(d) == 0
-    for call in (_fwd, _bwd, _step):
+    for call in (_fwd, _bwd) + ((_step,) if "seq_len" not in kw else ()):
         assert call(d) == binding.LSTM_ERR_UNSUPPORTED
 
 
