@@ -9,14 +9,14 @@
 // one accumulator collect them.  g^-I stays below e^40 by I* = floor(40 /
 // |log g|) (for out, not for X, decays below e^-40 act as e^-40); past I* the
 // state's true share is below e^-20 of its size, 2e-9, far below the output's
-// bf16 step.  X is
-// float32 and stays in its owners' registers during a walk: U is read from
-// tensor memory and added, and X's bf16 copy goes to shared memory as the next
-// chunk's operand.  The weighted values w c enter U's product split in four
-// bf16 parts, which hold all of float32, so the carried state is what float32
-// products give; the scores and the state enter the outputs' products rounded
-// once to bf16, as out itself is.  X is kept transposed, a
-// thread per value column, so that states are read and written coalesced.
+// bf16 step.  X is float32 and stays in its owners' registers during a walk: U
+// is read from tensor memory and added, and X's bf16 copy goes to shared memory
+// as the next chunk's operand.  The weighted values w c enter U's product split
+// in four bf16 parts, which hold all of float32, so the carried state is what
+// float32 products give (2.5e-7 of it off; 1.5e-6 with two parts); the scores
+// and the state enter the outputs' products rounded once to bf16, as out itself
+// is.  X is kept transposed, a thread per value column, so that states are read
+// and written coalesced.
 //
 // Chunks end where the row's valid steps end, whatever the direction: the one
 // partial chunk lies before time 0, where TMA fills zeros, and padded steps
@@ -31,12 +31,15 @@
 //   warps 12-15 (a thread per value column) weight c, 32 steps at a time;
 //   warps 16-19 (a thread per value column) carry X.
 // Tensor memory: P (P' over it; two of them for value sizes up to 64) | out | U
-// | w c (sets of 32 steps).
+// | w c (two sets of 32 steps).
 //
-// Bound: HBM (four rows of 2 d bytes a step).  A chunk's products take an
-// eighth of its load time on the tensor cores; what has to fit beside the
-// loads are the element passes, some 2000 issue slots of each of an SM's four
-// schedulers for 128 steps, and the hand-overs between them.
+// Bound: HBM (four rows of 2 d bytes a step; 1.5 us of an SM's share for 128
+// steps of 64).  The products keep the tensor pipe busy for 0.7 us of that (M =
+// 128 runs at N / 2 cycles an MMA).  What a chunk takes is 2.4 us: the seven
+// programs share each scheduler, and their element passes and hand-overs run at
+// the pace at which instructions arrive (32767 steps, 16 heads of 64: 70 us for
+// the outputs, DRAM at 41 %, tensor pipe at 34 %; with one program for scores
+// and outputs 20 % slower, with their loops unrolled 40 %).
 #include <cuda.h>
 
 #include <algorithm>
