@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
     const bool va = can_vec<T>(a, J.lda, J.da), vb = can_vec<T>(b, J.ldb, J.da), vc = can_vec<T>(c, J.ldc, J.dc);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int da4 = (J.da + 3) & ~3;
+    // of sizes 65 to 128 only the larger may fill the second half of a tile
+    const bool a2 = NW > 1 && J.da > 16 * W, c2 = NW > 1 && J.dc > 16 * W;
 
     if (threadIdx.x <= C) gp[threadIdx.x] = expf(it.ld * (float)threadIdx.x);
     for (int i = threadIdx.x; i < D * D; i += kThreads) {
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int u = 0; u < NW; ++u) {
+                            if (u && !c2) continue;
                             float z[W];
                             lds<W>(sx + (k + q) * P + u * 16 * W + tx * W, z);
 #pragma unroll
@@ -188,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int u = 0; u < NW; ++u) {
+                            if (u && !c2) continue;
                             float y[W];
                             lds<W>(sc + (k + q) * P + u * 16 * W + tx * W, y);
 #pragma unroll
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
                 }
             }
         }
+        if (!it.fin && tau + C >= it.tau1) break;   // nothing reads the last X
         // X <- g^m X + sum_j bscale g^(m-e-j) b_j^T c_j; rows like the columns
         float acc[NW][W][NW][W];
         const float gm = gp[m];
@@ -234,13 +239,17 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 1 : 3) lin_kernel(const _
                 for (int i = 0; i < W; ++i) x[t][i] *= f;
             }
 #pragma unroll
-            for (int t = 0; t < NW; ++t)
+            for (int t = 0; t < NW; ++t) {
+                if (t && !a2) continue;
 #pragma unroll
-                for (int i = 0; i < W; ++i)
+                for (int u = 0; u < NW; ++u) {
+                    if (u && !c2) continue;
 #pragma unroll
-                    for (int u = 0; u < NW; ++u)
+                    for (int i = 0; i < W; ++i)
 #pragma unroll
                         for (int j = 0; j < W; ++j) acc[t][i][u][j] = fmaf(x[t][i], y[u][j], acc[t][i][u][j]);
+                }
+            }
         }
         __syncthreads();   // every thread has read the old X
 #pragma unroll
