@@ -285,7 +285,13 @@ struct Chunks {
     }
 };
 
-template <bool HALF, int DA>
+// ENDS: every item forms U in its last chunk, with no test.  Without it, the
+// last chunk of a product whose last state nobody asked for forms none: of
+// the two chunks of 256 steps a half (forward and backward of 32 rows, 8 heads
+// of 128, lengths 128 to 256: 86.6 -> 82.8 us).  The test costs where chunks
+// are many: one row of 32767 steps, 16 heads of 64, in segments 121 -> 127 us,
+// so segments have ENDS.
+template <bool HALF, int DA, bool ENDS>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     lin_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     using Cf = Cfg<HALF, DA>;
@@ -527,17 +533,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
         } else if (warp == 2) {
             // ------------------------------------------------------------ U
-            int n = 0;
+            int n = 0, nu = 0;   // chunk, U
             Chunks k(digits);
             bool ok = true;
             for (; ok && k.next(p, digits); ++n) {
                 const int s = n % S;
+                if (!ENDS && k.c + 1 == k.w.c1 && p.g.job[k.w.job].fin == nullptr) {
+                    if (!wait(&full[s], n / S)) break;
+                    if (lane == 0) tc::mbar_arrive(&empty[s]);
+                    __syncwarp();
+                    continue;
+                }
                 const uint64_t db = tc::smem_desc_sw128_mn(tc::smem_u32(smem + s * Cf::STAGE) + Cf::A_BYTES, 16384);
                 const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.job].da) | (1u << 16);
-                if (!wait(&full[s], n / S) || (n > 0 && !wait(bUf, n - 1))) break;
+                if (!wait(&full[s], n / S) || (nu > 0 && !wait(bUf, nu - 1))) break;
 #pragma unroll 1
                 for (int r = 0; r < kC / kSub; ++r) {
-                    const int set = r % SETS, turn = n * (kC / kSub / SETS) + r / SETS;
+                    const int set = r % SETS, turn = nu * (kC / kSub / SETS) + r / SETS;
                     if (!wait(&bW[set], turn)) { ok = false; break; }
                     tc::tc_fence_after();
                     if (tc::elect_one()) {
@@ -555,6 +567,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     }
                     __syncwarp();
                 }
+                ++nu;
             }
             if (*abort_flag) {
                 const uint64_t t0 = globaltimer_ns();
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int row = ((lane >> 4) << 3) + (lane & 7), unit = ((col & 63) >> 3) + ((lane >> 3) & 1);
         const uint32_t lm = tc::smem_u32(smem) + 2 * Cf::A_BYTES + (uint32_t)((col >> 6) * 16384 + row * 128);
         const uint32_t u0 = (uint32_t)((unit ^ (row & 7)) << 4), u1 = (uint32_t)(((unit + 2) ^ (row & 7)) << 4);
-        int n = 0;
+        int n = 0, nu = 0;   // chunk, U
         bool ok = true;
         Walk w(digits);
         while (ok && w.next(p, digits)) {
@@ -763,13 +776,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             tc::named_bar_sync(2, 128);
             bool good = true;
-            for (int c = w.c0; c < w.c1 && good; ++c, ++n) {
+            const int c1 = ENDS || p.g.job[w.job].fin != nullptr ? w.c1 : w.c1 - 1;   // (an item of no chunks walks none)
+            for (int c = w.c0; c < c1 && good; ++c, ++n, ++nu) {
                 const uint32_t* wj = sw + (rev && c == w.nct - 1 ? 3 * kC / 2 : 0) + (lane & 3) * 4;
                 const int s = n % S;
                 if (!wait(&full[s], n / S)) { good = false; break; }
 #pragma unroll 1
                 for (int b = 0; b < kC / kSub; ++b) {
-                    const int set = b % SETS, turn = n * (kC / kSub / SETS) + b / SETS;
+                    const int set = b % SETS, turn = nu * (kC / kSub / SETS) + b / SETS;
                     const uint32_t src = lm + (uint32_t)(s * Cf::STAGE + b * kSub * 128);
                     // [lane half][8 registers: columns of 8 steps, rows 0-7 and 8-15 of the half]
                     uint32_t x[2][8];
@@ -829,6 +843,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     if (lane == 0) tc::mbar_arrive(&bW[set]);
                 }
             }
+            if (!ENDS && w.c0 < w.c1 && c1 < w.c1) {
+                // (a wait that skipped a phase would take an older one for its own)
+                good = good && wait(&full[n % S], n / S);
+                ++n;
+            }
             if (tc::named_bar_or(2, 128, !good)) ok = false;
         }
     } else {
@@ -838,7 +857,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int r = HALF ? (l & 63) : l;          // value column
         const bool second = HALF && l >= 64;        // the second parts' sums
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16) + Cf::cU;
-        int n = 0;
+        int n = 0, nu = 0;   // chunk, U
         bool ok = true;
         Walk w(digits);
         while (ok && w.next(p, digits)) {
@@ -891,10 +910,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             };
             bool good = true;
             if (outs && w.c0 < w.c1) good = put_x();
-            for (int c = w.c0; c < w.c1 && good; ++c) {
+            const int c1 = ENDS || p.g.job[w.job].fin != nullptr ? w.c1 : w.c1 - 1;
+            for (int c = w.c0; c < c1 && good; ++c) {
                 const int m = c == (J.reverse ? w.nct - 1 : 0) ? kC - w.pad : kC;
                 const float gm = expf(ld * (float)m);
-                if (!wait(bU, n)) { good = false; break; }
+                if (!wait(bU, nu)) { good = false; break; }
                 tc::tc_fence_after();
 #pragma unroll
                 for (int kb = 0; kb < DA; kb += 32) {
@@ -909,8 +929,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bUf);
                 ++n;
+                ++nu;
                 if (outs && c + 1 < w.c1) good = put_x();   // the next chunk's
             }
+            if (!ENDS && w.c0 < w.c1 && c1 < w.c1) ++n;
             if (fin) {
                 if constexpr (HALF) {
                     // the two sums are added in the place of X's copies, once
@@ -981,14 +1003,19 @@ bool make_map(CUtensorMap* map, const LinArgs& g, const void* base, long long ld
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool HALF, int DA>
-cudaError_t run(const Maps& maps, const Params& p, cudaStream_t s) {
+template <bool HALF, int DA, bool ENDS>
+cudaError_t launch(const Maps& maps, const Params& p, cudaStream_t s) {
     using Cf = Cfg<HALF, DA>;
-    cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<HALF, DA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<HALF, DA, ENDS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Cf::SMEM);
     if (e != cudaSuccess) return e;
-    lin_tc_kernel<HALF, DA><<<std::min(p.items, p.g.num_sms), kThreadsTc, Cf::SMEM, s>>>(maps, p);
+    lin_tc_kernel<HALF, DA, ENDS><<<std::min(p.items, p.g.num_sms), kThreadsTc, Cf::SMEM, s>>>(maps, p);
     return cudaGetLastError();
+}
+
+template <bool HALF, int DA>
+cudaError_t run(const Maps& maps, const Params& p, cudaStream_t s) {
+    return p.mode != kLinWhole ? launch<HALF, DA, true>(maps, p, s) : launch<HALF, DA, false>(maps, p, s);
 }
 
 // All products of `a` whose sizes take the same kernel, one launch.
