@@ -94,7 +94,7 @@ struct Cfg {
     static constexpr int PARTS = HALF ? 2 : 4;             // operands that hold w c
     static constexpr int SETS = 2;                             // sets of 32 steps of them
     static constexpr int TAB_BYTES = (2 * 3 * kC / 2 + kTab) * 4;
-    static constexpr int BARS = 3 * S + 4 + 2 * SETS + 2 * XB + 2 * PB;
+    static constexpr int BARS = 4 * S + 4 + 2 * SETS + 2 * XB + 2 * PB;
     static constexpr size_t SMEM = (size_t)S * STAGE + XB * X_BYTES + TAB_BYTES + BARS * 8 + 48;
     // tensor-memory columns; a set of w c takes 16 of them for each operand
     static constexpr int cP = 0, cO = PB * 128, cU = cO + DCP, cW = cU + DA;
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint64_t* bUf = bU + 1;        // U read
     uint64_t* bX = bUf + 1;        // [XB] X written
     uint64_t* bM2 = bX + XB;       // [XB] a X computed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bM2 + XB);
+    uint64_t* bK = bM2 + XB;       // [S] the weighing warps have seen a chunk without U
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bK + S);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* ended = reinterpret_cast<volatile int*>(tmem_slot + 2);   // warps that are done
     int* digits = reinterpret_cast<int*>(tmem_slot + 3);   // [8]: the first item's, gridDim.x's
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], outs ? 2 : 1);
             tc::mbar_init(&bS[s], 4);
+            tc::mbar_init(&bK[s], 4);
         }
         for (int i = 0; i < PB; ++i) {
             tc::mbar_init(&bP[i], 1);
@@ -535,12 +537,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         } else if (warp == 2) {
             // ------------------------------------------------------------ U
             int n = 0, nu = 0;   // chunk, U
+            uint32_t seen = 0;   // phase of each stage's bK
             Chunks k(digits);
             bool ok = true;
             for (; ok && k.next(p, digits); ++n) {
                 const int s = n % S;
                 if (!ENDS && k.c + 1 == k.w.c1 && p.g.job[k.w.job].fin == nullptr) {
-                    if (!wait(&full[s], n / S)) break;
+                    // nothing else of such a chunk waits for the weighing warps:
+                    // the stage stays until they have looked at it, so that
+                    // full[s] cannot run two phases ahead of them
+                    if (!wait(&full[s], n / S) || !wait(&bK[s], (int)(seen >> s))) break;
+                    seen ^= 1u << s;
                     if (lane == 0) tc::mbar_arrive(&empty[s]);
                     __syncwarp();
                     continue;
@@ -847,6 +854,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             if (!ENDS && w.c0 < w.c1 && c1 < w.c1) {
                 // (a wait that skipped a phase would take an older one for its own)
                 good = good && wait(&full[n % S], n / S);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bK[n % S]);
                 ++n;
             }
             if (tc::named_bar_or(2, 128, !good)) ok = false;
