@@ -100,7 +100,10 @@ struct Cfg {
     static constexpr int cP = 0, cO = PB * 128, cU = cO + DCP, cW = cU + DA;
     static_assert(cW + SETS * PARTS * kSub / 2 <= 512, "tensor memory");
 };
-static_assert(Cfg<false, 128>::SMEM <= 232448, "shared memory of one block");
+// (the largest is value sizes up to 64 with key sizes up to 128)
+constexpr size_t kSmemMost = 232448;   // of one block
+static_assert(Cfg<false, 64>::SMEM <= kSmemMost && Cfg<false, 128>::SMEM <= kSmemMost, "shared memory of one block");
+static_assert(Cfg<true, 64>::SMEM <= kSmemMost && Cfg<true, 128>::SMEM <= kSmemMost, "shared memory of one block");
 
 // The decay that the outputs are formed with, and I*.
 __device__ __forceinline__ float out_decay(float ld) { return ld < -40.0f ? -40.0f : ld; }
