@@ -396,8 +396,9 @@ lstm_status lstm_layer_norm_backward(const lstm_norm_desc* desc, const void* gra
  * The tensors must not overlap.  A tensor with numel 0 is skipped; its
  * entries may be NULL.  With num_tensors 0 only the step counter moves.
  * LSTM_ERR_INVALID_ARG: a NULL array or entry, a pointer off its type's
- * alignment, state_bits other than 8 or 32, lr, eps or weight_decay negative
- * or not finite, eps 0, beta1 or beta2 outside [0, 1).
+ * alignment, state_bits other than 8 or 32, lr or weight_decay negative or not
+ * finite, lr / (1 - beta1) or lr weight_decay beyond float32's range, eps
+ * outside [2^-126, 2^126], beta1 or beta2 outside [0, 1).
  */
 typedef struct {
     int num_tensors;

@@ -1,6 +1,7 @@
 // C-ABI entry points of the operators beside the LSTM (include/lstm.h,
 // "Operators beside the LSTM"): argument checks on the host, then the
 // kernels' launchers under the library's kernel timing.
+#include <float.h>
 #include <math.h>
 
 #include <mutex>
@@ -29,11 +30,17 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 // A required pointer to elements of `a` bytes.
 bool given(const void* p, size_t a) { return p && aligned(p, a); }
 bool finite_ge0(double x) { return isfinite(x) && x >= 0.0; }
+// The kernel's own values: it takes them rounded to float32.
+bool float_ge0(double x) { return x >= 0.0 && x <= (double)FLT_MAX; }
 
 bool valid(const lstm_adamw_desc* d) {
     return d && d->num_tensors >= 0 && (d->grad_dtype == LSTM_F32 || d->grad_dtype == LSTM_BF16) &&
            (d->state_bits == 8 || d->state_bits == 32) && finite_ge0(d->lr) && d->beta1 >= 0.0 && d->beta1 < 1.0 &&
-           d->beta2 >= 0.0 && d->beta2 < 1.0 && finite_ge0(d->eps) && d->eps > 0.0 && finite_ge0(d->weight_decay);
+           d->beta2 >= 0.0 && d->beta2 < 1.0 && finite_ge0(d->weight_decay) &&
+           // the largest step size and decay the kernel forms; an infinite one times a zero moment is NaN
+           float_ge0(d->lr / (1.0 - d->beta1)) && float_ge0(d->lr * d->weight_decay) &&
+           // what a zero second moment leaves under the quotient: its reciprocal has to be a number, not 0
+           d->eps >= (double)FLT_MIN && d->eps <= 0x1p126;
 }
 
 bool valid(const lstm_norm_desc* d) {
