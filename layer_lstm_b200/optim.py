@@ -68,7 +68,12 @@ class AdamW:
                 s["v_scale"] if eight else None)
 
     def _addresses(self):
-        a = [None if t is None else t.data_ptr() for ts in self._lists() if ts is not None for t in ts]
+        a = []
+        for ts in self._lists():
+            if ts is self.copies:   # (entries may be None)
+                a += [t is not None and t.data_ptr() for t in ts or ()]
+            elif ts is not None:
+                a += map(torch.Tensor.data_ptr, ts)
         a.append(self.state["step"].data_ptr())
         if self.scalars is not None:
             a.append(self.scalars.data_ptr())
