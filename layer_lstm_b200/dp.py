@@ -46,7 +46,9 @@ class GradBucket:
     problem (order: every dW_ih, every dW_hh, every db_ih).
 
     `adopt(prob)` points the problem's gradient tensors at views of the
-    buffer, so that the library writes the gradients straight into it.  db_hh
+    buffer, so that the library writes the gradients straight into it; the
+    tensors it held before share the views' storage from then on, so that an
+    optimizer made with them reads the bucket too.  db_hh
     equals db_ih (the two biases enter the gates as a sum), so only db_ih is
     exchanged; `finish()` copies the reduced db_ih into db_hh."""
 
@@ -65,6 +67,8 @@ class GradBucket:
     def adopt(cls, prob, bias: bool) -> "GradBucket":
         grads = list(prob.dw_ih) + list(prob.dw_hh) + (list(prob.db_ih) if bias else [])
         b = cls(grads)
+        for t, view in zip(grads, b.views):
+            t.data = view
         n = len(prob.dw_ih)
         prob.dw_ih = b.views[:n]
         prob.dw_hh = b.views[n:2 * n]

@@ -93,9 +93,9 @@ class DeviceProblem:
             binding.check(self.backward(stream), "lstm_backward")
 
     def optimizer(self, **kw):
-        """optim.AdamW over this problem's weights and biases and the gradients its backward writes
-        (make it after dp.GradBucket.adopt, which moves the gradients).  bf16 weights are updated
-        through float32 masters that the optimizer holds; the weights become their rounded copies."""
+        """optim.AdamW over this problem's weights and biases and the gradients its backward writes (in a
+        dp.GradBucket or not).  bf16 weights are updated through float32 masters that the optimizer
+        holds; the weights become their rounded copies."""
         from .optim import AdamW
         params = self.w_ih + self.w_hh + (self.b_ih + self.b_hh if self.wl.bias else [])
         grads = self.dw_ih + self.dw_hh + (self.db_ih + self.db_hh if self.wl.bias else [])
