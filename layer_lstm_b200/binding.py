@@ -3,14 +3,13 @@
 Argument marshalling only: tensors become device pointers, lists of tensors
 become host arrays of device pointers, and every function returns the C
 status code.  All computation happens in the CUDA library; there is no other
-code path.  PyTorch is used by callers for device memory and streams.
+code path.  PyTorch is used by callers for device memory and streams; calls
+with plain addresses and a stream handle do without it.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-
-import torch
 
 from . import build as _build
 
@@ -206,6 +205,7 @@ def _parr(ts):
 
 def _stream(stream):
     if stream is None:
+        import torch
         # the handle alone: torch.cuda.current_stream() builds an object around it (3.4 us of a 13 us call)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
@@ -332,7 +332,7 @@ def lstm_adamw_read_state(desc, numel, m, v, m_scale, v_scale, m_out, v_out, str
     return load().lstm_adamw_read_state(ctypes.byref(desc), n, *a, _stream(stream))
 
 
-_TORCH_DTYPE = {LSTM_F32: torch.float32, LSTM_BF16: torch.bfloat16}
+_TYPES = {}   # torch's types by name or code, known once a call brings a tensor
 
 
 def _fits(t, numel, dtype, device):
@@ -348,6 +348,10 @@ def _device(*ts):
     addresses."""
     for t in ts:
         if t is not None and not isinstance(t, int):
+            if not _TYPES:
+                import torch
+                _TYPES.update({LSTM_F32: torch.float32, LSTM_BF16: torch.bfloat16, "f32": torch.float32,
+                               "i32": torch.int32})
             return t.get_device()
     return None
 
@@ -357,7 +361,10 @@ def _call(device, stream, f, *args):
     there, on `stream` or that device's current stream.  Tensors that are not on a GPU are refused."""
     if device is not None and device < 0:
         return LSTM_ERR_INVALID_ARG
-    if device is None or device == torch.cuda.current_device():
+    if device is None:
+        return f(*args, _stream(stream))
+    import torch
+    if device == torch.cuda.current_device():
         return f(*args, _stream(stream))
     with torch.cuda.device(device):
         return f(*args, _stream(stream))
@@ -370,7 +377,8 @@ def lstm_layer_norm_workspace_size(desc: lstm_norm_desc) -> int:
 def lstm_layer_norm_forward(desc, x, weight, bias, y, mean=None, rstd=None, stream=None) -> int:
     """Tensors whose type, device, size or contiguity does not match the description are refused
     (LSTM_ERR_INVALID_ARG); plain device addresses pass as they are."""
-    rows, cols, dt, dev, f32 = desc.rows, desc.cols, _TORCH_DTYPE.get(desc.dtype), _device(x, y), torch.float32
+    rows, cols, dev = desc.rows, desc.cols, _device(x, y)
+    dt, f32 = _TYPES.get(desc.dtype), _TYPES.get("f32")
     if not (_fits(x, rows * cols, dt, dev) and _fits(y, rows * cols, dt, dev) and _fits(weight, cols, dt, dev)
             and _fits(bias, cols, dt, dev) and _fits(mean, rows, f32, dev) and _fits(rstd, rows, f32, dev)):
         return LSTM_ERR_INVALID_ARG
@@ -380,8 +388,8 @@ def lstm_layer_norm_forward(desc, x, weight, bias, y, mean=None, rstd=None, stre
 
 def lstm_layer_norm_backward(desc, grad_y, x, weight, mean, rstd, dx, dweight, dbias, workspace=None, stream=None,
                              ws_bytes=None) -> int:
-    rows, cols, dt, f32 = desc.rows, desc.cols, _TORCH_DTYPE.get(desc.dtype), torch.float32
-    n, dev = rows * cols, _device(grad_y, x, dweight)
+    rows, cols, dev = desc.rows, desc.cols, _device(grad_y, x, dweight)
+    n, dt, f32 = rows * cols, _TYPES.get(desc.dtype), _TYPES.get("f32")
     if not (_fits(grad_y, n, dt, dev) and _fits(x, n, dt, dev) and _fits(dx, n, dt, dev)
             and _fits(weight, cols, dt, dev) and _fits(mean, rows, f32, dev) and _fits(rstd, rows, f32, dev)
             and _fits(dweight, cols, f32, dev) and _fits(dbias, cols, f32, dev)
@@ -417,7 +425,7 @@ def _fits_rows(t, desc, size, ld, dtype, device):
 
 
 def _attention_fits(desc, dev, lengths, log_decay, qs, ks, vs, outs, states, workspace=None):
-    dt, f32 = _TORCH_DTYPE.get(desc.dtype), torch.float32
+    dt, f32 = _TYPES.get(desc.dtype), _TYPES.get("f32")
     dk, dv = desc.key_size, desc.value_size
     n = desc.batch * desc.heads * dk * dv
     for ts, size, ld in ((qs, dk, desc.ld_q), (ks, dk, desc.ld_k), (vs, dv, desc.ld_v), (outs, dv, 0)):
@@ -427,7 +435,7 @@ def _attention_fits(desc, dev, lengths, log_decay, qs, ks, vs, outs, states, wor
     for t in states:
         if not _fits(t, n, f32, dev):
             return False
-    return (_fits(log_decay, desc.heads, f32, dev) and _fits(lengths, desc.batch, torch.int32, dev)
+    return (_fits(log_decay, desc.heads, f32, dev) and _fits(lengths, desc.batch, _TYPES.get("i32"), dev)
             and _device(workspace) in (None, dev))
 
 
