@@ -344,8 +344,8 @@ def _fits(t, numel, dtype, device):
 
 
 def _device(*ts):
-    """Index of the GPU of the first tensor among the arguments (-1: a CPU tensor); None when all are plain
-    addresses."""
+    """Index of the GPU of the first tensor among a call's arguments (-1: a CPU tensor); None when all are
+    plain addresses."""
     for t in ts:
         if t is not None and not isinstance(t, int):
             if not _TYPES:
@@ -377,7 +377,7 @@ def lstm_layer_norm_workspace_size(desc: lstm_norm_desc) -> int:
 def lstm_layer_norm_forward(desc, x, weight, bias, y, mean=None, rstd=None, stream=None) -> int:
     """Tensors whose type, device, size or contiguity does not match the description are refused
     (LSTM_ERR_INVALID_ARG); plain device addresses pass as they are."""
-    rows, cols, dev = desc.rows, desc.cols, _device(x, y)
+    rows, cols, dev = desc.rows, desc.cols, _device(x, y, weight, bias, mean, rstd)
     dt, f32 = _TYPES.get(desc.dtype), _TYPES.get("f32")
     if not (_fits(x, rows * cols, dt, dev) and _fits(y, rows * cols, dt, dev) and _fits(weight, cols, dt, dev)
             and _fits(bias, cols, dt, dev) and _fits(mean, rows, f32, dev) and _fits(rstd, rows, f32, dev)):
@@ -388,7 +388,7 @@ def lstm_layer_norm_forward(desc, x, weight, bias, y, mean=None, rstd=None, stre
 
 def lstm_layer_norm_backward(desc, grad_y, x, weight, mean, rstd, dx, dweight, dbias, workspace=None, stream=None,
                              ws_bytes=None) -> int:
-    rows, cols, dev = desc.rows, desc.cols, _device(grad_y, x, dweight)
+    rows, cols, dev = desc.rows, desc.cols, _device(grad_y, x, weight, mean, rstd, dx, dweight, dbias, workspace)
     n, dt, f32 = rows * cols, _TYPES.get(desc.dtype), _TYPES.get("f32")
     if not (_fits(grad_y, n, dt, dev) and _fits(x, n, dt, dev) and _fits(dx, n, dt, dev)
             and _fits(weight, cols, dt, dev) and _fits(mean, rows, f32, dev) and _fits(rstd, rows, f32, dev)
@@ -443,7 +443,7 @@ def lstm_linear_attention_forward(desc, q, k, v, log_decay, s0, out, s_n, worksp
                                   lengths=None) -> int:
     """Tensors that do not match the description (type, device, size, layout) are refused with
     LSTM_ERR_INVALID_ARG; plain device addresses pass as they are."""
-    dev = _device(q, log_decay)
+    dev = _device(q, k, v, log_decay, s0, out, s_n, workspace, lengths)
     if not _attention_fits(desc, dev, lengths, log_decay, (q,), (k,), (v,), (out,), (s0, s_n), workspace):
         return LSTM_ERR_INVALID_ARG
     return _call(dev, stream, load().lstm_linear_attention_forward, ctypes.byref(desc), _p(lengths), _p(q), _p(k),
@@ -453,7 +453,7 @@ def lstm_linear_attention_forward(desc, q, k, v, log_decay, s0, out, s_n, worksp
 
 def lstm_linear_attention_backward(desc, q, k, v, log_decay, s0, grad_out, grad_sn, dq, dk, dv, ds0, workspace,
                                    stream=None, ws_bytes=None, lengths=None) -> int:
-    dev = _device(q, log_decay)
+    dev = _device(q, k, v, log_decay, s0, grad_out, grad_sn, dq, dk, dv, ds0, workspace, lengths)
     if not _attention_fits(desc, dev, lengths, log_decay, (q, dq), (k, dk), (v, dv), (grad_out,),
                            (s0, grad_sn, ds0), workspace):
         return LSTM_ERR_INVALID_ARG
@@ -463,7 +463,7 @@ def lstm_linear_attention_backward(desc, q, k, v, log_decay, s0, grad_out, grad_
 
 
 def lstm_linear_attention_step(desc, q, k, v, log_decay, state, out, stream=None, lengths=None) -> int:
-    dev = _device(q, log_decay)
+    dev = _device(q, k, v, log_decay, state, out, lengths)
     if not _attention_fits(desc, dev, lengths, log_decay, (q,), (k,), (v,), (out,), (state,)):
         return LSTM_ERR_INVALID_ARG
     return _call(dev, stream, load().lstm_linear_attention_step, ctypes.byref(desc), _p(lengths), _p(q), _p(k), _p(v),
