@@ -344,7 +344,8 @@ lstm_status lstm_linear_attention_step(const lstm_attention_desc* desc, const in
  * be NULL where not wanted; what is wanted is overwritten.  The sums over
  * rows have a fixed order.  The workspace (256-byte aligned, size from the
  * query) holds the row groups' sums and is needed for dweight or dbias only.
- * y may be x and dx may be grad_y or x (in place); no other overlap.
+ * y may be x and dx may be grad_y or x (in place); no other overlap.  Rows of
+ * more than 2^30 columns return LSTM_ERR_UNSUPPORTED.
  */
 typedef struct {
     long long rows;   /* >= 0; 0 gives dweight = dbias = 0 */
@@ -353,7 +354,8 @@ typedef struct {
     float eps;        /* >= 0, finite */
 } lstm_norm_desc;
 
-/* Workspace bytes of lstm_layer_norm_backward; 0 if the description is invalid. */
+/* Workspace bytes of lstm_layer_norm_backward; 0 if the description is invalid
+ * or unsupported. */
 size_t lstm_layer_norm_workspace_size(const lstm_norm_desc* desc);
 
 lstm_status lstm_layer_norm_forward(const lstm_norm_desc* desc, const void* x, const void* weight,

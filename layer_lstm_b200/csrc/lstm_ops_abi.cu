@@ -47,6 +47,8 @@ bool valid(const lstm_norm_desc* d) {
     return d && d->rows >= 0 && d->cols >= 1 && (d->dtype == LSTM_F32 || d->dtype == LSTM_BF16) &&
            isfinite(d->eps) && d->eps >= 0.0f;
 }
+// (columns are counted in 32 bits, a block's stride past the last one included)
+bool supported(const lstm_norm_desc* d) { return d->cols <= 1 << 30; }
 
 bool valid(const lstm_attention_desc* d) {
     if (!d || d->batch < 0 || d->seq_len < 0 || d->heads < 1 || d->key_size < 1 || d->value_size < 1) return false;
@@ -177,7 +179,7 @@ lstm_status lstm_adamw_read_state(const lstm_adamw_desc* desc, const long long* 
 }
 
 size_t lstm_layer_norm_workspace_size(const lstm_norm_desc* desc) {
-    if (!valid(desc)) return 0;
+    if (!valid(desc) || !supported(desc)) return 0;
     // the partition of the largest device this library runs on serves where no device is at hand
     const int sms = num_sms();
     const size_t n = (size_t)norm_partials(desc->rows, desc->cols, sms > 0 ? sms : 148);
@@ -187,6 +189,7 @@ size_t lstm_layer_norm_workspace_size(const lstm_norm_desc* desc) {
 lstm_status lstm_layer_norm_forward(const lstm_norm_desc* desc, const void* x, const void* weight,
                                     const void* bias, void* y, float* mean, float* rstd, cudaStream_t stream) {
     if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    if (!supported(desc)) return LSTM_ERR_UNSUPPORTED;
     const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
     if (!aligned(weight, e) || !aligned(bias, e) || !aligned(mean, 4) || !aligned(rstd, 4))
         return LSTM_ERR_INVALID_ARG;
@@ -205,6 +208,7 @@ lstm_status lstm_layer_norm_backward(const lstm_norm_desc* desc, const void* gra
                                      float* dweight, float* dbias, void* workspace, size_t ws_bytes,
                                      cudaStream_t stream) {
     if (!valid(desc)) return LSTM_ERR_INVALID_ARG;
+    if (!supported(desc)) return LSTM_ERR_UNSUPPORTED;
     const size_t e = desc->dtype == LSTM_F32 ? 4 : 2;
     if (!aligned(weight, e) || !aligned(dx, e) || !aligned(dweight, 4) || !aligned(dbias, 4))
         return LSTM_ERR_INVALID_ARG;
