@@ -287,11 +287,13 @@ lstm_status lstm_noalloc_query_status(cudaStream_t stream);
  * cores in float32.
  * A NaN or an infinity in a step's inputs may reach the outputs of earlier
  * steps of the same chunk of up to 128.
- * Sizes from 1 to 128 for key_size and value_size, up to 2^30 steps; larger
- * ones return LSTM_ERR_UNSUPPORTED.  Workspace (256-byte aligned) from the query; it
- * serves forward and backward, is filled and read within a call, and holds
- * the call's status word (lstm_query_status).  Beyond s_n over s0, no output
- * may overlap an input or another output.
+ * Sizes from 1 to 128 for key_size and value_size, up to 2^30 steps and 2^30
+ * for heads * size; larger ones return LSTM_ERR_UNSUPPORTED.  Workspace
+ * (256-byte aligned) from the query; it serves forward and backward, is filled
+ * and read within a call, and holds the call's status word
+ * (lstm_query_status; a call with batch 0 enqueues nothing and leaves the word
+ * as it is).  Beyond s_n over s0, no output may overlap an input or another
+ * output.
  */
 typedef struct {
     int batch;        /* >= 0 */

@@ -59,9 +59,11 @@ bool valid(const lstm_attention_desc* d) {
     if ((long long)d->batch * d->heads > (1ll << 28)) return false;
     return (d->ld_q == 0 || d->ld_q >= wk) && (d->ld_k == 0 || d->ld_k >= wk) && (d->ld_v == 0 || d->ld_v >= wv);
 }
-// (steps are counted in 32 bits, a chunk or a segment past the last one included)
+// (steps are counted in 32 bits, a chunk or a segment past the last one
+// included, and so is a head's place in its row)
 bool supported(const lstm_attention_desc* d) {
-    return d->key_size <= kLinMaxDim && d->value_size <= kLinMaxDim && d->seq_len <= 1 << 30;
+    return d->key_size <= kLinMaxDim && d->value_size <= kLinMaxDim && d->seq_len <= 1 << 30 &&
+           (long long)d->heads * (d->key_size > d->value_size ? d->key_size : d->value_size) <= 1ll << 30;
 }
 
 DType dtype_of(lstm_dtype t) { return t == LSTM_F32 ? DType::F32 : DType::BF16; }
