@@ -132,27 +132,27 @@ class AdamW:
         binding.check(st, "lstm_adamw_step")
 
     def read_state(self, m_out=None, v_out=None, stream=None):
-        """The moments as two flat float32 tensors, every parameter's after the one before."""
+        """The moments as two flat float32 tensors, every parameter's after the one before, written on
+        `stream` (default: the current stream of the tensors' device; what is not given is that stream's)."""
         self._follow()
         total = sum(self._numel)
-        if m_out is None:
-            m_out = torch.empty(total, device=self.device)
-        if v_out is None:
-            v_out = torch.empty(total, device=self.device)
-        for name, t in (("m_out", m_out), ("v_out", v_out)):
-            _check(name, t, torch.float32, self.device, total)
-        if self.desc.state_bits == 32:
-            with torch.cuda.device(self.device):
-                s = torch.cuda.current_stream() if stream is None else stream
-                s = torch.cuda.ExternalStream(s) if isinstance(s, int) else s
-                with torch.cuda.stream(s):
+        with torch.cuda.device(self.device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            s = torch.cuda.ExternalStream(s) if isinstance(s, int) else s
+            with torch.cuda.stream(s):
+                if m_out is None:
+                    m_out = torch.empty(total, device=self.device)
+                if v_out is None:
+                    v_out = torch.empty(total, device=self.device)
+                for name, t in (("m_out", m_out), ("v_out", v_out)):
+                    _check(name, t, torch.float32, self.device, total)
+                if self.desc.state_bits == 32:
                     for out, ts in ((m_out, self.state["m"]), (v_out, self.state["v"])):
                         if ts:
                             torch.cat([t.reshape(-1) for t in ts], out=out)
-            return m_out, v_out
-        outs = [(ctypes.c_void_p * len(self.params))(*[t.data_ptr() + 4 * at for at in self._at])
-                for t in (m_out, v_out)]
-        with torch.cuda.device(self.device):
-            st = binding.lstm_adamw_read_state(self.desc, self._numel, *self._ptr[3:], *outs, stream)
+                    return m_out, v_out
+                outs = [(ctypes.c_void_p * len(self.params))(*[t.data_ptr() + 4 * at for at in self._at])
+                        for t in (m_out, v_out)]
+                st = binding.lstm_adamw_read_state(self.desc, self._numel, *self._ptr[3:], *outs, s)
         binding.check(st, "lstm_adamw_read_state")
         return m_out, v_out
