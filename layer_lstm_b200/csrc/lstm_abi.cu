@@ -55,9 +55,11 @@ DevInfo device_info() {
 // makes that block of every FFMA or float32 tensor-core forward (backward)
 // recurrent launch withhold its arrival of that step, so the blocks of its group give up at their next
 // counter wait (no copy is in flight there) and the call ends with
-// LSTM_ERR_TIMEOUT in the status word.
+// LSTM_ERR_TIMEOUT in the status word.  "att:<block>:<chunk>": that block of
+// every tensor-core linear-attention launch withholds the weighed values of its
+// chunk of that number (counted over its items), with the same end.
 struct SkipArrival {
-    int fwd_block = -1, fwd_step = -1, bwd_block = -1, bwd_step = -1;
+    int fwd_block = -1, fwd_step = -1, bwd_block = -1, bwd_step = -1, att_block = -1, att_chunk = -1;
 };
 
 const SkipArrival& skip_arrival() {
@@ -70,6 +72,7 @@ const SkipArrival& skip_arrival() {
             if (sscanf(e, "%3[a-z]:%d:%d", which, &blk, &st) == 3 && blk >= 0 && st >= 0) {
                 if (strcmp(which, "fwd") == 0) { r.fwd_block = blk; r.fwd_step = st; }
                 if (strcmp(which, "bwd") == 0) { r.bwd_block = blk; r.bwd_step = st; }
+                if (strcmp(which, "att") == 0) { r.att_block = blk; r.att_chunk = st; }
             }
         }
         return r;
@@ -474,6 +477,11 @@ unsigned long long* trace_for(int kind, int steps, cudaStream_t s) {
 }
 
 uint64_t wait_limit_ns() { return timeout_ns(); }
+
+void lin_skip(int* block, int* chunk) {
+    *block = skip_arrival().att_block;
+    *chunk = skip_arrival().att_chunk;
+}
 
 cudaError_t timed_op(OpKind kind, cudaStream_t s, cudaError_t (*launch)(const void*, cudaStream_t, int*),
                      const void* args) {

@@ -71,6 +71,7 @@ struct Params {
     int reset;                          // first launch of a call: the status word starts anew
     int* status;
     uint64_t timeout_ns;
+    int skip_block, skip_chunk;         // this block's weighing warps withhold this chunk's arrivals (a test; -1: none)
 };
 
 struct alignas(64) Maps {
@@ -367,7 +368,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (uint32_t)(phase & 1), abort_flag); };
+    // A warp gives up as a whole: a lane that left alone would leave the others
+    // in front of a warp-wide instruction.
+    auto poll = [&](uint64_t* bar, int phase) { return wait_phase(bar, (uint32_t)(phase & 1), abort_flag); };
+    auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, poll(bar, phase)) != 0; };
+    auto wait2 = [&](uint64_t* bar, int phase, uint64_t* bar2, int phase2) {
+        return __all_sync(0xffffffffu, poll(bar, phase) && poll(bar2, phase2)) != 0;
+    };
     // descriptor of `d` moved by `bytes`
     auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
 
@@ -378,7 +385,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             // (the whole warp waits, one lane issues: a wait by one lane of a
             // diverged warp takes 600 cycles, by the warp 100)
             auto wait_timed = [&](uint64_t* bar, int phase) {
-                return tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status, p.timeout_ns);
+                return __all_sync(0xffffffffu, tc::mbar_wait(bar, (uint32_t)(phase & 1), abort_flag, p.status,
+                                                             p.timeout_ns)) != 0;
             };
             int n = 0;
             Chunks k(digits);
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 // with two score buffers the next chunk's product runs beside this chunk's P'
                 if (PB == 2 && ((n > 0 && !wait(bO, n - 1)) || !scores())) break;
                 // out's accumulator already holds a X
-                if (!wait(&bM2[n % XB], n / XB) || !wait(&bPb[n % PB], n / PB)) break;
+                if (!wait2(&bM2[n % XB], n / XB, &bPb[n % PB], n / PB)) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
 #pragma unroll 2
@@ -519,7 +527,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 const uint64_t da = tc::smem_desc_sw128(tc::smem_u32(smem + s * Cf::STAGE));
                 const uint64_t dx = tc::smem_desc_sw128(tc::smem_u32(sX + (n % XB) * Cf::X_BYTES));
                 const uint32_t id = tc::instr_desc(1, 128, J.dc);
-                if (!wait(&full[s], n / S) || !wait(&bX[n % XB], n / XB) || (n > 0 && !wait(bOf, n - 1))) break;
+                // (the phase before the first counts as ended)
+                if (!__all_sync(0xffffffffu, poll(&full[s], n / S) && poll(&bX[n % XB], n / XB) && poll(bOf, n + 1))) break;
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
 #pragma unroll 1
@@ -549,7 +558,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     // nothing else of such a chunk waits for the weighing warps:
                     // the stage stays until they have looked at it, so that
                     // full[s] cannot run two phases ahead of them
-                    if (!wait(&full[s], n / S) || !wait(&bK[s], (int)(seen >> s))) break;
+                    if (!wait2(&full[s], n / S, &bK[s], (int)(seen >> s))) break;
                     seen ^= 1u << s;
                     if (lane == 0) tc::mbar_arrive(&empty[s]);
                     __syncwarp();
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                 }
                 const uint64_t db = tc::smem_desc_sw128_mn(tc::smem_u32(smem + s * Cf::STAGE) + Cf::A_BYTES, 16384);
                 const uint32_t id = tc::instr_desc(1, 128, p.g.job[k.w.job].da) | (1u << 16);
-                if (!wait(&full[s], n / S) || (nu > 0 && !wait(bUf, nu - 1))) break;
+                if (!wait2(&full[s], n / S, bUf, nu + 1)) break;   // (the phase before the first counts as ended)
 #pragma unroll 1
                 for (int r = 0; r < kC / kSub; ++r) {
                     const int set = r % SETS, turn = nu * (kC / kSub / SETS) + r / SETS;
@@ -757,6 +766,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const int row = ((lane >> 4) << 3) + (lane & 7), unit = ((col & 63) >> 3) + ((lane >> 3) & 1);
         const uint32_t lm = tc::smem_u32(smem) + 2 * Cf::A_BYTES + (uint32_t)((col >> 6) * 16384 + row * 128);
         const uint32_t u0 = (uint32_t)((unit ^ (row & 7)) << 4), u1 = (uint32_t)(((unit + 2) ^ (row & 7)) << 4);
+        const int skip = (int)blockIdx.x == p.skip_block ? p.skip_chunk : -1;
         int n = 0, nu = 0;   // chunk, U
         bool ok = true;
         Walk w(digits);
@@ -851,7 +861,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                     tc::tmem_st_wait();
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bW[set]);
+                    if (lane == 0 && n != skip) tc::mbar_arrive(&bW[set]);
                 }
             }
             if (!ENDS && w.c0 < w.c1 && c1 < w.c1) {
@@ -1073,6 +1083,8 @@ cudaError_t run_mode(const LinArgs& a, int mode, cudaStream_t s, int* n) {
             p.reset = *n == 0;
             p.status = a.status;
             p.timeout_ns = a.timeout_ns;
+            p.skip_block = a.skip_block;
+            p.skip_chunk = a.skip_chunk;
             cudaError_t e = half ? (da == 64 ? run<true, 64>(maps, p, s) : run<true, 128>(maps, p, s))
                                  : (da == 64 ? run<false, 64>(maps, p, s) : run<false, 128>(maps, p, s));
             if (e != cudaSuccess) return e;

@@ -122,6 +122,7 @@ struct LinArgs {
     int from_end;                   // segments are counted from the valid steps' end (see lin_steps)
     int* status;
     uint64_t timeout_ns;
+    int skip_block, skip_chunk;     // fault injection of a test (-1: none), see skip_arrival
     int num_sms;
 };
 // Parts the time axis is cut into for njobs products; 1: none.  `tc`: for the
@@ -136,6 +137,8 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t s, int* n);
 
 // Limit of a bounded wait (lstm_query_status).
 uint64_t wait_limit_ns();
+// The block and chunk of LSTM_B200_DEBUG_SKIP_ARRIVAL="att:<block>:<chunk>", -1 without it.
+void lin_skip(int* block, int* chunk);
 
 struct LinStepArgs {
     int B, H, dk, dv;

@@ -79,6 +79,7 @@ LinArgs lin_args(const lstm_attention_desc* d, const int* lengths, const float* 
     a.status = static_cast<int*>(ws);
     a.buf = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
     a.timeout_ns = wait_limit_ns();
+    lin_skip(&a.skip_block, &a.skip_chunk);
     a.num_sms = num_sms();
     return a;
 }
