@@ -10,6 +10,7 @@ compute in bf16, written to their bf16 tensors too.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 
 import torch
@@ -25,8 +26,26 @@ def _check(name, t, dtype, device, numel):
         raise ValueError(f"{name}: need a contiguous {dtype} tensor of {numel} elements on {device}")
 
 
+def _span(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+def _check_apart(written, read):
+    """The tensors of `written` share no memory with one another or with those of `read`."""
+    spans = sorted(_span(t) for t in written if t.numel())
+    for (_, end), (start, _) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError("parameters, copies and moments may not share memory")
+    for t in read:
+        start, end = _span(t)
+        i = bisect.bisect_left(spans, (end,))   # the spans that begin before its end
+        if t.numel() and i and spans[i - 1][1] > start:
+            raise ValueError("a gradient may not share memory with what a step writes")
+
+
 class AdamW:
-    """params: float32 tensors; grads: as many float32 or bf16 tensors (one type) of the same sizes.
+    """params: float32 tensors; grads: as many float32 or bf16 tensors (one type) of the same sizes.  What a
+    step writes may not share memory (a weight used twice is given once).
 
     copies: bf16 tensors (or None entries) that receive the updated parameters.  state_bits: 32, or 8
     (codes in blocks of 256 elements; see include/lstm.h).  scalars: float32 device tensor of two, the
@@ -105,6 +124,8 @@ class AdamW:
             for i, k in enumerate(sizes):
                 _check(f"{name}[{i}]", state[name][i], dt, device, -(-k // div))
         _check("step", state["step"], torch.int64, device, 1)
+        _check_apart([t for ts in self._lists() if ts is not None and ts is not self.grads for t in ts if t is not None]
+                     + [state["step"]], self.grads)
         self.desc.num_tensors = n
         self.desc.grad_dtype = binding.LSTM_F32 if gdt == torch.float32 else binding.LSTM_BF16
         self._numel = binding._numels(sizes)
