@@ -26,20 +26,19 @@ def _check(name, t, dtype, device, numel):
         raise ValueError(f"{name}: need a contiguous {dtype} tensor of {numel} elements on {device}")
 
 
-def _span(t):
-    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+def _spans(ts):
+    return [(at, at + n) for at, n in ((t.data_ptr(), t.nbytes) for t in ts) if n]
 
 
 def _check_apart(written, read):
     """The tensors of `written` share no memory with one another or with those of `read`."""
-    spans = sorted(_span(t) for t in written if t.numel())
+    spans = sorted(_spans(written))
     for (_, end), (start, _) in zip(spans, spans[1:]):
         if start < end:
             raise ValueError("parameters, copies and moments may not share memory")
-    for t in read:
-        start, end = _span(t)
+    for start, end in _spans(read):
         i = bisect.bisect_left(spans, (end,))   # the spans that begin before its end
-        if t.numel() and i and spans[i - 1][1] > start:
+        if i and spans[i - 1][1] > start:
             raise ValueError("a gradient may not share memory with what a step writes")
 
 
