@@ -283,10 +283,13 @@ lstm_status lstm_noalloc_query_status(cudaStream_t stream);
  * (with 16-byte aligned arrays, rows in multiples of 8 elements, and heads *
  * size at least 64) run on the tensor cores: there the scores and the state
  * are rounded to bf16 as operands of out's products (not of the state's), and
- * a decay below e^-40 acts as e^-40 in out.  Everything else runs on the CUDA
- * cores in float32.
- * A NaN or an infinity in a step's inputs may reach the outputs of earlier
- * steps of the same chunk of up to 128.
+ * a decay below e^-40 acts as e^-40 in out.  There the scores (q_t . k_j, and
+ * grad_out_t . v_j in the backward) are multiplied by up to e^40, or by
+ * exp(128 |log_decay|) where that is less, before the decay is taken out again:
+ * scores beyond 1e21 in magnitude may give infinities where the result is
+ * finite.  Everything else runs on the CUDA cores in float32.
+ * A NaN or an infinity in a step's inputs may reach the outputs and gradients
+ * of the other steps of the same chunk of up to 128.
  * Sizes from 1 to 128 for key_size and value_size, up to 2^30 steps and 2^30
  * for heads * size; larger ones return LSTM_ERR_UNSUPPORTED.  Workspace
  * (256-byte aligned) from the query; it serves forward and backward, is filled

@@ -31,8 +31,11 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return v;
 }
 
-// One block per row, for rows too wide for a block's registers: the row is
-// read again for each pass over it.
+// One block per row, for rows too wide for a block's registers (from 16385
+// columns in bf16, 8193 in float32, 4097 where rows are not 16-byte multiples):
+// the row is read again for each pass over it, an element a thread, mostly from
+// L2.  1024 x 32768 bf16: 88 us forward (1.5 TB/s), 427 backward (0.5); 4096 x
+// 4097: 36 and 99.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormFwdArgs a) {
     __shared__ float red[kThreads / 32];
@@ -146,13 +149,15 @@ __global__ void __launch_bounds__(kAddThreads) norm_add_kernel(const float* part
 // ------------------------------------------------------------ rows in registers
 // A row is held by a group of G threads, PER values each, and read once: W
 // consecutive values per load (16 bytes, or 1 where rows are not 16-byte
-// multiples), loads G * W columns apart.  PER is 64
-// bytes of packed elements (8 elements otherwise): what a row costs beside its
-// elements, some 120 instructions of sums over the group, root and addresses,
-// is then a third of it.  (With 32 bytes, 8192 x 2048 bf16 forward and backward
-// took 47 us instead of 40.)  The backward keeps a row and two column sums in
-// registers, one block of 256 an SM; the forward two.  A block of at least 256
-// threads takes 256 / G rows at a time.
+// multiples), loads G * W columns apart.  PER is 64 bytes of packed elements (8
+// elements otherwise): what a row costs beside its elements, some 120
+// instructions of sums over the group, root and addresses, is then a third of
+// it.  (With 32 bytes, 8192 x 2048 bf16 forward and backward took 47 us instead
+// of 40.)  The backward keeps a row and two column sums in registers, one block
+// of 256 an SM; the forward two.  A block of at least 256 threads takes 256 / G
+// rows at a time.  Blocks of 512 threads have 128 registers each: the backward
+// of the widest bf16 rows, 8193 to 16384 columns, spills (1024 x 16384: 71 us,
+// 1.4 TB/s; 8192 x 2048: 32 us, 3.2 TB/s).
 template <typename T, int W>
 constexpr int per_of() { return W == 1 ? 8 : sizeof(T) == 2 ? 32 : 16; }
 
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(block_of(G), kFwdThreads / block_of(G)) norm_f
 }
 
 // dx, and the block's sums of dw and db over its rows: every thread keeps the
-// sums of its own 16 columns in registers, the groups are added at the end.
+// sums of its own kPer columns in registers, the groups are added at the end.
 template <typename T, int G, int W>
 __global__ void __launch_bounds__(block_of(G), 1) norm_bwd_rows_kernel(const NormBwdArgs a) {
     constexpr int kPer = per_of<T, W>();
